@@ -1,4 +1,5 @@
-"""Python binding of libqgemm (quantized GEMMs dequantized inside the kernel).
+"""Python binding of libqgemm (quantized GEMMs dequantized inside the kernel,
+and the paged key-value cache of a decode step).
 
 Argument marshalling only: each function checks dtypes and shapes of torch
 tensors, allocates outputs with torch, and calls the C entry point of the same
@@ -51,6 +52,12 @@ _SIGNATURES = [
     ("qgemm_mxfp4_act", ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P]),
     ("qgemm_fp8_act", ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     ("qgemm_fp8_act_noalloc", ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    ("qgemm_kv_plan", ctypes.c_int, [_P] * 8 + [_I64] * 6 + [_P]),
+    ("qgemm_kv_append", ctypes.c_int,
+     [ctypes.c_int, ctypes.c_int] + [_P] * 7 + [_I64] * 12 + [_P]),
+    ("qgemm_paged_attention_workspace_bytes", ctypes.c_int64, [_I64] * 6),
+    ("qgemm_paged_attention", ctypes.c_int,
+     [ctypes.c_int, ctypes.c_int] + [_P] * 9 + [_I64] * 15 + [ctypes.c_float, _P]),
     ("qgemm_read_probe", ctypes.c_int, [_P, _I64, _P, _I64, _P]),
     ("qgemm_mfma_probe", ctypes.c_int, [ctypes.c_int, _P, _I64, _P, _I64, _P]),
 ]
@@ -418,6 +425,187 @@ def qgemm_fp8_act_noalloc(a, b_packed, scale_b, N, out):
     out = _out(out, M, N, torch.bfloat16, a.device)
     _check(lib().qgemm_fp8_act_noalloc(_ptr(a), _ptr(b_packed), _ptr(scale_b), _ptr(out), M, N,
                                        K, _stream(a)), "qgemm_fp8_act_noalloc")
+    return out
+
+
+# ---- paged key-value cache ---------------------------------------------------
+
+# qgemm_dtype codes; uint8 holds e4m3fn codes, as qgemm_quantize_fp8 returns them
+_HALF_TYPES = {torch.float16: 1, torch.bfloat16: 2}
+_CACHE_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.uint8: 3}
+
+
+def _view(t, dtypes, ndim, name):
+    """A device tensor of one of `dtypes` whose last axis is dense; the other
+    axes may have any strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"the last axis of {name} must be dense")
+
+
+def _strides(t):
+    """Strides of all axes but the last; 0 where an axis has one entry or none,
+    whose stride torch leaves arbitrary."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride())]
+
+
+def _same_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+
+
+def _kv_pools(k_cache, v_cache, k_scale, v_scale, dtype):
+    """Check both pools; returns (type code, [pages, kv_heads, page_size, dim],
+    strides of the first three axes)."""
+    _view(k_cache, _CACHE_TYPES, 4, "k_cache")
+    _view(v_cache, _CACHE_TYPES, 4, "v_cache")
+    shape, strides = k_cache.shape, _strides(k_cache)
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != shape or _strides(v_cache) != strides:
+        raise ValueError("k_cache and v_cache must agree in type, shape and strides")
+    code = _CACHE_TYPES[k_cache.dtype]
+    if code == 3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise ValueError(f"an e4m3 cache needs {name} (float32, one per kv head)")
+            _need(t, torch.float32, 1, name)
+            if t.shape[0] != shape[1]:
+                raise ValueError(f"{name} must have {shape[1]} entries, one per kv head")
+    else:
+        if k_cache.dtype != dtype:
+            raise TypeError(f"a 16-bit cache must be {dtype} like the tokens, got {k_cache.dtype}")
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a 16-bit cache takes no scales")
+    if shape[2] < 1:
+        raise ValueError("pages must hold at least one token")
+    return code, shape, strides
+
+
+def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None):
+    """Pages and slots for the tokens that enter a step, on the device.
+
+    Request b holds cached[b] tokens and gains added[b].  table (int32
+    [batch, width]) gets the pages that it gains from free_pages (int32), in
+    place.  Returns (lens [batch], cu_tokens [batch + 1], cu_pages
+    [batch + 1], all int32, and slots int64 [tokens]); `out` may be a tuple of
+    those four tensors to write into.  tokens: how many tokens the host counts
+    on (the sum of added).  cu_pages[-1] is the number of pages taken; past
+    the end of free_pages entries and slots become -1."""
+    _view(table, (torch.int32,), 2, "table")
+    batch, width = table.shape
+    for t, name in ((cached, "cached"), (added, "added")):
+        _need(t, torch.int32, 1, name)
+        if t.shape[0] != batch:
+            raise ValueError(f"{name} must have {batch} entries, one per request")
+    _need(free_pages, torch.int32, 1, "free_pages")
+    if page_size < 1 or tokens < 0:
+        raise ValueError("page_size must be at least 1 and tokens at least 0")
+    sizes = ((torch.int32, batch), (torch.int32, batch + 1), (torch.int32, batch + 1),
+             (torch.int64, tokens))
+    if out is None:
+        out = tuple(torch.empty(n, dtype=d, device=table.device) for d, n in sizes)
+    else:
+        out = tuple(out)
+        if len(out) != 4:
+            raise ValueError("out must be (lens, cu_tokens, cu_pages, slots)")
+        for t, (d, n), name in zip(out, sizes, ("lens", "cu_tokens", "cu_pages", "slots")):
+            _need(t, d, 1, name)
+            if t.shape[0] != n:
+                raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    _same_device(table, cached, added, free_pages, *out)
+    _check(lib().qgemm_kv_plan(table.data_ptr(), cached.data_ptr(), added.data_ptr(),
+                               free_pages.data_ptr(), *(t.data_ptr() for t in out), batch, width,
+                               _strides(table)[0], free_pages.shape[0], page_size, tokens,
+                               _stream(table)), "qgemm_kv_plan")
+    return out
+
+
+def qgemm_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
+    """Write new tokens' keys and values ([tokens, kv_heads, dim] views, fp16
+    or bf16) into the slots (int64 [tokens]; page * page_size + offset, below
+    0: skipped) of the pools [pages, kv_heads, page_size, dim], in place.
+    Pools of the same type take a copy; float8_e4m3fn (or uint8 code) pools
+    take e4m3fn(x / scale[head]), k_scale and v_scale float32 [kv_heads]."""
+    _view(k, _HALF_TYPES, 3, "k")
+    _view(v, (k.dtype,), 3, "v")
+    _need(slots, torch.int64, 1, "slots")
+    code, (pages, kv_heads, page_size, dim), strides = _kv_pools(k_cache, v_cache, k_scale,
+                                                                v_scale, k.dtype)
+    tokens = slots.shape[0]
+    if tuple(k.shape) != (tokens, kv_heads, dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{tokens}, {kv_heads}, {dim}], got {list(k.shape)} "
+                         f"and {list(v.shape)}")
+    _same_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    _check(lib().qgemm_kv_append(
+        _HALF_TYPES[k.dtype], code, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if code == 3 else None,
+        v_scale.data_ptr() if code == 3 else None, tokens, kv_heads, dim, *_strides(k),
+        *_strides(v), pages, page_size, *strides, _stream(k)), "qgemm_kv_append")
+
+
+def qgemm_paged_attention_workspace_bytes(batch, heads, kv_heads, dim, max_len, window=0):
+    n = lib().qgemm_paged_attention_workspace_bytes(int(batch), int(heads), int(kv_heads),
+                                                    int(dim), int(max_len), int(window))
+    if n < 0:
+        raise QgemmError(int(n), "qgemm_paged_attention_workspace_bytes")
+    return n
+
+
+def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scale=None, window=0,
+                          max_len=None, scale=None, out=None, workspace=None):
+    """Attention of one new token per request over its cached tokens.
+
+    q: [batch, heads, dim] view, fp16 or bf16; the pools as in qgemm_kv_append
+    with heads a multiple of kv_heads; table int32 [batch, width]; lens int32
+    [batch], the tokens of each request, the new one included.  window > 0
+    keeps the last `window` tokens of each.  max_len bounds lens on the host
+    (default: what the table can name); scale defaults to dim ** -0.5.
+    workspace: uint8, at least qgemm_paged_attention_workspace_bytes(batch,
+    heads, kv_heads, dim, max_len, window); allocated if None.  Returns out,
+    [batch, heads, dim] of q's type."""
+    _view(q, _HALF_TYPES, 3, "q")
+    code, (pages, kv_heads, page_size, dim), strides = _kv_pools(k_cache, v_cache, k_scale,
+                                                                v_scale, q.dtype)
+    batch, heads = q.shape[:2]
+    if q.shape[2] != dim:
+        raise ValueError(f"q has head size {q.shape[2]}, the cache {dim}")
+    if kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} heads do not divide over {kv_heads} kv heads")
+    _view(table, (torch.int32,), 2, "table")
+    _need(lens, torch.int32, 1, "lens")
+    if table.shape[0] != batch or lens.shape[0] != batch:
+        raise ValueError(f"table and lens must have {batch} rows, one per request")
+    width = table.shape[1]
+    if max_len is None:
+        max_len = min(width * page_size, 2 ** 31 - 1)
+    need = qgemm_paged_attention_workspace_bytes(batch, heads, kv_heads, dim, max_len, window)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace, torch.uint8, 1, "workspace")
+        if workspace.shape[0] < need:
+            raise ValueError(f"workspace needs {need} bytes")
+    if out is None:
+        out = torch.empty((batch, heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        _need(out, q.dtype, 3, "out")
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    _same_device(q, k_cache, v_cache, table, lens, k_scale, v_scale, workspace, out)
+    _check(lib().qgemm_paged_attention(
+        _HALF_TYPES[q.dtype], code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        table.data_ptr(), lens.data_ptr(), k_scale.data_ptr() if code == 3 else None,
+        v_scale.data_ptr() if code == 3 else None, out.data_ptr(), workspace.data_ptr(), batch,
+        heads, kv_heads, dim, *_strides(q), pages, page_size, *strides, width, _strides(table)[0],
+        max_len, window, dim ** -0.5 if scale is None else scale, _stream(q)),
+        "qgemm_paged_attention")
     return out
 
 

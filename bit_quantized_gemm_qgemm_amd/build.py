@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["decode_gemm.hip", "tile_gemm.hip", "tile_wo256.hip", "tile_mx256.hip", "quantize.hip",
-           "prepack.hip", "probes.hip",
+           "prepack.hip", "probes.hip", "kv_cache.hip", "paged_attention.hip",
            "api.cpp"]
 
 HIPCC_FLAGS = [

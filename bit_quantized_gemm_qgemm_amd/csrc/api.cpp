@@ -5,6 +5,7 @@
 
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/qgemm.h"
@@ -267,6 +268,54 @@ int scratch_of_current_device(uint8_t** out) {
   return QGEMM_OK;
 }
 
+// ---- paged key-value cache ---------------------------------------------------
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;   // elements; keeps offsets far from 2^63
+
+bool below(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v < hi; }
+
+// Types of the cache calls: 16-bit elements, pools of the same type or e4m3
+// with both scale arrays (and only then).
+int check_kv_types(int dtype, int cache_dtype, const float* k_scale, const float* v_scale,
+                   int64_t kv_heads) {
+  if (dtype != QGEMM_F16 && dtype != QGEMM_BF16) return QGEMM_ERR_FORMAT;
+  if (cache_dtype != dtype && cache_dtype != QGEMM_E4M3) return QGEMM_ERR_FORMAT;
+  if (cache_dtype == QGEMM_E4M3) {
+    if (!present(k_scale, kv_heads) || !present(v_scale, kv_heads)) return QGEMM_ERR_NULL;
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return QGEMM_ERR_ALIGN;
+  } else if (k_scale || v_scale) {
+    return QGEMM_ERR_FORMAT;
+  }
+  return QGEMM_OK;
+}
+
+bool kv_dim_ok(int64_t dim) { return dim >= 16 && dim <= 256 && dim % 16 == 0; }
+
+// Rows of the pools counted in 32 bits (see KvPool).
+int check_kv_pool(int64_t kv_heads, int64_t dim, int64_t pages, int64_t page_size,
+                  int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                  qgemm::KvPool* pool) {
+  if (!kv_dim_ok(dim)) return QGEMM_ERR_SHAPE;
+  if (!below(kv_heads, 0, kMaxIndex) || !below(pages, 0, kMaxIndex) ||
+      !below(page_size, 1, kMaxIndex))
+    return QGEMM_ERR_SHAPE;
+  for (int64_t st : {page_stride, head_stride, token_stride})
+    if (!below(st, 0, kMaxIndex * dim) || st % dim != 0) return QGEMM_ERR_SHAPE;
+  const int64_t pr = page_stride / dim, hr = head_stride / dim, tr = token_stride / dim;
+  if (pages > 0 && kv_heads > 0) {   // each product is below 2^62
+    const int64_t a = (pages - 1) * pr, b = (kv_heads - 1) * hr, c = (page_size - 1) * tr;
+    if (a >= kMaxIndex || b >= kMaxIndex || c >= kMaxIndex || a + b + c >= kMaxIndex)
+      return QGEMM_ERR_SHAPE;
+  }
+  *pool = qgemm::KvPool{(int)pages, (int)page_size, (int)pr, (int)hr, (int)tr};
+  return QGEMM_OK;
+}
+
+bool kv_view_ok(int64_t outer, int64_t inner) {   // strides of q, k, v: whole 16-byte pieces
+  return below(outer, 0, kMaxStride) && below(inner, 0, kMaxStride) && outer % 8 == 0 &&
+         inner % 8 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -498,6 +547,144 @@ int qgemm_fp8_act_noalloc(const float* a, const void* b_packed, const float* sca
   uint8_t* ws = nullptr;
   if ((st = scratch_of_current_device(&ws)) != QGEMM_OK) return st;
   return fp8_act_run(a, b_packed, scale_b, c, ws, M, N, K, stream);
+}
+
+// ---- paged key-value cache ---------------------------------------------------
+
+int qgemm_kv_plan(int32_t* table, const int32_t* cached, const int32_t* added,
+                  const int32_t* free_pages, int32_t* lens, int32_t* cu_tokens,
+                  int32_t* cu_pages, int64_t* slots, int64_t batch, int64_t width,
+                  int64_t table_stride, int64_t num_free, int64_t page_size, int64_t tokens,
+                  void* stream) {
+  if (!below(batch, 0, kMaxIndex) || !below(width, 0, kMaxIndex) ||
+      !below(num_free, 0, kMaxIndex) || !below(page_size, 1, kMaxIndex) ||
+      !below(tokens, 0, kMaxIndex) || !below(table_stride, 0, kMaxStride) ||
+      (batch > 1 && table_stride < width))
+    return QGEMM_ERR_SHAPE;
+  if (!present(table, batch * width) || !present(cached, batch) || !present(added, batch) ||
+      !present(free_pages, num_free) || !present(lens, batch) || !cu_tokens || !cu_pages ||
+      !present(slots, tokens))
+    return QGEMM_ERR_NULL;
+  for (const void* p : {(const void*)table, (const void*)cached, (const void*)added,
+                        (const void*)free_pages, (const void*)lens, (const void*)cu_tokens,
+                        (const void*)cu_pages})
+    if (!aligned(p, 4)) return QGEMM_ERR_ALIGN;
+  if (!aligned(slots, 8)) return QGEMM_ERR_ALIGN;
+  int st = check_device();
+  if (st != QGEMM_OK) return st;
+  return launched(qgemm::launch_kv_plan(
+      qgemm::KvPlan{table, cached, added, free_pages, lens, cu_tokens, cu_pages, slots, batch,
+                    width, table_stride, num_free, page_size, tokens},
+      as_stream(stream)));
+}
+
+int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
+                    const int64_t* slots, void* k_cache, void* v_cache, const float* k_scale,
+                    const float* v_scale, int64_t tokens, int64_t kv_heads, int64_t dim,
+                    int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                    int64_t v_head_stride, int64_t pages, int64_t page_size, int64_t page_stride,
+                    int64_t head_stride, int64_t token_stride, void* stream) {
+  int st = check_kv_types(dtype, cache_dtype, k_scale, v_scale, kv_heads);
+  if (st != QGEMM_OK) return st;
+  qgemm::KvPool pool;
+  if ((st = check_kv_pool(kv_heads, dim, pages, page_size, page_stride, head_stride, token_stride,
+                          &pool)) != QGEMM_OK)
+    return st;
+  if (!below(tokens, 0, kMaxIndex) || !kv_view_ok(k_token_stride, k_head_stride) ||
+      !kv_view_ok(v_token_stride, v_head_stride))
+    return QGEMM_ERR_SHAPE;
+  const bool some = tokens > 0 && kv_heads > 0;
+  if (!present(k, some) || !present(v, some) || !present(slots, tokens) ||
+      !present(k_cache, some && pages > 0) || !present(v_cache, some && pages > 0))
+    return QGEMM_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16))
+    return QGEMM_ERR_ALIGN;
+  if (!some || pages == 0) return QGEMM_OK;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  qgemm::KvAppend a{};
+  a.x[0] = k;
+  a.x[1] = v;
+  a.cache[0] = k_cache;
+  a.cache[1] = v_cache;
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.token_stride[0] = k_token_stride;
+  a.token_stride[1] = v_token_stride;
+  a.head_stride[0] = k_head_stride;
+  a.head_stride[1] = v_head_stride;
+  a.slots = slots;
+  a.tokens = tokens;
+  a.kv_heads = (int)kv_heads;
+  a.dim = (int)dim;
+  a.pool = pool;
+  return launched(qgemm::launch_kv_append(dtype, cache_dtype, a, as_stream(stream)));
+}
+
+int64_t qgemm_paged_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t kv_heads,
+                                              int64_t dim, int64_t max_len, int64_t window) {
+  if (!below(batch, 0, kMaxIndex) || !below(heads, 0, kMaxIndex) ||
+      !below(kv_heads, 1, kMaxIndex) || heads % kv_heads != 0 || !kv_dim_ok(dim) ||
+      !below(max_len, 0, kMaxIndex) || !below(window, 0, kMaxIndex) ||
+      batch * heads >= kMaxIndex)
+    return QGEMM_ERR_SHAPE;
+  return qgemm::paged_attention_workspace(batch, heads, kv_heads, dim, max_len, window);
+}
+
+int qgemm_paged_attention(int dtype, int cache_dtype, const void* q, const void* k_cache,
+                          const void* v_cache, const int32_t* table, const int32_t* lens,
+                          const float* k_scale, const float* v_scale, void* out,
+                          void* workspace, int64_t batch, int64_t heads, int64_t kv_heads,
+                          int64_t dim, int64_t q_batch_stride, int64_t q_head_stride,
+                          int64_t pages, int64_t page_size, int64_t page_stride,
+                          int64_t head_stride, int64_t token_stride, int64_t width,
+                          int64_t table_stride, int64_t max_len, int64_t window, float scale,
+                          void* stream) {
+  int st = check_kv_types(dtype, cache_dtype, k_scale, v_scale, kv_heads);
+  if (st != QGEMM_OK) return st;
+  const int64_t need =
+      qgemm_paged_attention_workspace_bytes(batch, heads, kv_heads, dim, max_len, window);
+  if (need < 0) return (int)need;
+  qgemm::KvPool pool;
+  if ((st = check_kv_pool(kv_heads, dim, pages, page_size, page_stride, head_stride, token_stride,
+                          &pool)) != QGEMM_OK)
+    return st;
+  if (!kv_view_ok(q_batch_stride, q_head_stride) || !below(width, 0, kMaxIndex) ||
+      !below(table_stride, 0, kMaxStride) || (batch > 1 && table_stride < width))
+    return QGEMM_ERR_SHAPE;
+  const int64_t rows = batch * heads;
+  if (!present(q, rows) || !present(out, rows) || !present(lens, rows) ||
+      !present(table, rows > 0 ? width : 0) || !present(k_cache, rows > 0 ? pages : 0) ||
+      !present(v_cache, rows > 0 ? pages : 0) || !present(workspace, need))
+    return QGEMM_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4))
+    return QGEMM_ERR_ALIGN;
+  if (rows == 0) return QGEMM_OK;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  qgemm::PagedAttention a{};
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.table = table;
+  a.lens = lens;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.out = out;
+  a.workspace = workspace;
+  a.q_batch_stride = q_batch_stride;
+  a.q_head_stride = q_head_stride;
+  a.table_stride = table_stride;
+  a.batch = (int)batch;
+  a.heads = (int)heads;
+  a.kv_heads = (int)kv_heads;
+  a.dim = (int)dim;
+  a.pool = pool;
+  a.limit = max_len < width * page_size ? max_len : width * page_size;
+  if (pages == 0) a.limit = 0;   // every page is missing
+  a.window = window;
+  a.scale = scale;
+  return launched(qgemm::launch_paged_attention(dtype, cache_dtype, a, as_stream(stream)));
 }
 
 int qgemm_read_probe(const void* buf, int64_t bytes, uint32_t* sink, int64_t workgroups,

@@ -202,6 +202,56 @@ hipError_t launch_fp8_256(const void* a, const void* b_packed, const float* scal
                           const float* scale_b, void* c, int64_t M, int64_t N, int64_t K,
                           hipStream_t stream);
 
+// ---- paged key-value cache (kv_cache.hip, paged_attention.hip) --------------
+
+// Where the rows (one token of one kv head, dim elements) of both pools lie.
+// Strides and the row count are in rows, so a row's number fits 32 bits and
+// its byte offset is formed in 64 where it is used.
+struct KvPool {
+  int pages, page_size;
+  int page_rows, head_rows, token_rows;
+};
+
+struct KvAppend {
+  const void* x[2];        // new keys, values
+  void* cache[2];          // their pools
+  const float* scale[2];   // e4m3 only, per kv head
+  int64_t token_stride[2], head_stride[2];   // of x, in elements
+  const int64_t* slots;
+  int64_t tokens;
+  int kv_heads, dim;
+  KvPool pool;
+};
+// elements of dtype (1 fp16, 2 bf16), pools of cache_dtype (dtype or 3 e4m3)
+hipError_t launch_kv_append(int dtype, int cache_dtype, const KvAppend& a, hipStream_t stream);
+
+struct KvPlan {
+  int32_t* table;
+  const int32_t *cached, *added, *free_pages;
+  int32_t *lens, *cu_tokens, *cu_pages;
+  int64_t* slots;
+  int64_t batch, width, table_stride, num_free, page_size, tokens;
+};
+hipError_t launch_kv_plan(const KvPlan& p, hipStream_t stream);
+
+struct PagedAttention {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *table, *lens;
+  const float *k_scale, *v_scale;   // e4m3 only, per kv head
+  void* out;
+  void* workspace;
+  int64_t q_batch_stride, q_head_stride, table_stride;
+  int batch, heads, kv_heads, dim;
+  KvPool pool;
+  int64_t limit;     // min(max_len, width * page_size)
+  int64_t window;    // 0: none
+  float scale;
+};
+int64_t paged_attention_workspace(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dim,
+                                  int64_t max_len, int64_t window);
+hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttention& a,
+                                  hipStream_t stream);
+
 // Streaming read of `bytes` bytes (a multiple of 16, buf 16-byte aligned) by
 // `workgroups` workgroups; one word per workgroup goes to sink.
 hipError_t launch_read_probe(const void* buf, int64_t bytes, uint32_t* sink, int64_t workgroups,

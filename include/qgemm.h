@@ -12,7 +12,8 @@
  * (qgemm_w4a16_grouped, qgemm_w8a16_grouped), NVFP4 weights with fp16
  * activations (qgemm_nvfp4), and MXFP4 / FP8 GEMMs that quantize fp32
  * activations on the device inside the call (qgemm_mxfp4_act,
- * qgemm_fp8_act).
+ * qgemm_fp8_act).  Next to them, the paged key-value cache of a decode step:
+ * qgemm_kv_plan, qgemm_kv_append and qgemm_paged_attention.
  *
  * Sources (short names):
  *   W4A16 page -- "Triton W4A16 blocked GEMM and Blackwell NVFP4"
@@ -312,6 +313,110 @@ int qgemm_w4a16_grouped(const void* x, const void* w_packed, void* y, int64_t M,
                         int64_t K, int64_t group_k, void* stream);
 int qgemm_w8a16_grouped(const void* x, const void* w_packed, void* y, int64_t M, int64_t N,
                         int64_t K, int64_t group_k, void* stream);
+
+/*
+ * Key-value cache of a serving loop: the attention between the QKV product
+ * and the output product of a decode step.
+ *
+ * Keys and values live in two pools of `pages` pages of page_size tokens,
+ *   k_cache, v_cache: [pages, kv_heads, page_size, dim] elements,
+ * in fp16 or bf16, or as e4m3fn codes with one fp32 scale per kv head (a
+ * stored value is code * k_scale[h]).  The order of the first three axes is
+ * free: page_stride, head_stride and token_stride (in elements, the same for
+ * both pools, each a multiple of dim) say where a page, head and token start,
+ * so a [pages, page_size, kv_heads, dim] pool and one half of a
+ * [pages, 2, kv_heads, page_size, dim] pool are read in place.  The slot of a
+ * token is page * page_size + offset.  A block table int32 [batch, width]
+ * (table_stride entries between rows) names the page of each page_size tokens
+ * of a request; an entry below 0 or at or above `pages` is a missing page.
+ *
+ * Differing from the conventions above: int32 arrays need 4-byte and int64
+ * arrays 8-byte alignment only; q, k and v may be strided views (strides in
+ * elements, multiples of 8), for instance the three parts of a fused QKV
+ * product.  dim is a multiple of 16 up to 256.  The pools may be of any size
+ * in bytes, with fewer than 2^31 rows of dim elements.
+ */
+enum qgemm_dtype {
+  QGEMM_F16 = 1,
+  QGEMM_BF16 = 2,
+  QGEMM_E4M3 = 3          /* e4m3fn codes: caches only                       */
+};
+
+/*
+ * qgemm_kv_plan -- give the tokens that enter a step their pages and slots.
+ *
+ * Request b holds cached[b] tokens and gains added[b] (negative counts are
+ * taken as 0).  With P = page_size:
+ *   lens[b]   = min(cached + added, width * P)      tokens after the step
+ *   have      = min(ceil(cached / P), width)        pages that it holds
+ *   take      = max(ceil(lens / P) - have, 0)       pages that it gains
+ *   cu_tokens [batch + 1], cu_pages [batch + 1]: sums of added and of take
+ *               over the requests before, the totals last
+ *   table[b, have + j] = free_pages[cu_pages[b] + j] for j < take, or -1 once
+ *               the list's num_free entries are used up (cu_pages[batch] >
+ *               num_free says so); other entries are left alone
+ *   slots[t]  = slot of token t, for t < tokens; the tokens of request b are
+ *               cu_tokens[b] .. cu_tokens[b + 1] - 1 at positions cached[b]
+ *               on.  -1 where t is past the last token, the position past
+ *               width * P or the page missing (a negative table entry).
+ * tokens is the length of slots, the sum of added that the host counts on; a
+ * device sum below or above it is handled as stated.  The sums are formed in
+ * 64 bits and stored as int32, so they should stay below 2^31.  One launch, no
+ * workspace.
+ */
+int qgemm_kv_plan(int32_t* table, const int32_t* cached, const int32_t* added,
+                  const int32_t* free_pages, int32_t* lens, int32_t* cu_tokens,
+                  int32_t* cu_pages, int64_t* slots, int64_t batch, int64_t width,
+                  int64_t table_stride, int64_t num_free, int64_t page_size, int64_t tokens,
+                  void* stream);
+
+/*
+ * qgemm_kv_append -- write the keys and values of `tokens` new tokens into
+ * their slots.  k, v: dtype (QGEMM_F16 or QGEMM_BF16) [tokens, kv_heads, dim]
+ * views.  cache_dtype is dtype (the elements are copied; k_scale and v_scale
+ * must be NULL) or QGEMM_E4M3: code = e4m3fn(fp32(x / scale[h])), nearest
+ * even, saturated at +-448, NaN kept (k_scale, v_scale: fp32 [kv_heads]).  A
+ * slot below 0 or at or above pages * page_size is skipped.  Slots must
+ * differ from one another: which token a slot named twice keeps is
+ * unspecified.
+ */
+int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
+                    const int64_t* slots, void* k_cache, void* v_cache, const float* k_scale,
+                    const float* v_scale, int64_t tokens, int64_t kv_heads, int64_t dim,
+                    int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                    int64_t v_head_stride, int64_t pages, int64_t page_size, int64_t page_stride,
+                    int64_t head_stride, int64_t token_stride, void* stream);
+
+/*
+ * qgemm_paged_attention -- attention of one new token per request over the
+ * paged cache: for request b and head h, with n = lens[b] held to 0 ..
+ * min(max_len, width * page_size) and t running over the tokens max(0, n -
+ * window) .. n - 1 (window 0: all n) whose page is not missing,
+ *   s[t] = scale * (q[b, h] . K[t]),   out[b, h] = sum_t softmax(s)[t] V[t],
+ * K and V of kv head h / (heads / kv_heads).  A request with no such token
+ * gets zeros.  Tokens that are left out are never used, whatever their memory
+ * holds.  q: dtype [batch, heads, dim] view; out: dtype [batch, heads, dim],
+ * dense; cache_dtype is dtype or QGEMM_E4M3 (then k_scale, v_scale are fp32
+ * [kv_heads], else NULL).  Products, softmax and sums are fp32 (the
+ * probabilities enter the matrix cores as the sum of two 16-bit parts), the
+ * output is rounded once.  max_len is a host-side bound of lens, which sizes
+ * the launch.
+ *
+ * workspace: qgemm_paged_attention_workspace_bytes(...) bytes, 16-byte
+ * aligned, of any contents; calls that share one must not overlap.  May be
+ * NULL where that size is 0.
+ */
+int64_t qgemm_paged_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t kv_heads,
+                                              int64_t dim, int64_t max_len, int64_t window);
+int qgemm_paged_attention(int dtype, int cache_dtype, const void* q, const void* k_cache,
+                          const void* v_cache, const int32_t* table, const int32_t* lens,
+                          const float* k_scale, const float* v_scale, void* out,
+                          void* workspace, int64_t batch, int64_t heads, int64_t kv_heads,
+                          int64_t dim, int64_t q_batch_stride, int64_t q_head_stride,
+                          int64_t pages, int64_t page_size, int64_t page_stride,
+                          int64_t head_stride, int64_t token_stride, int64_t width,
+                          int64_t table_stride, int64_t max_len, int64_t window, float scale,
+                          void* stream);
 
 /*
  * qgemm_read_probe -- measurement reference, not part of any GEMM: reads the

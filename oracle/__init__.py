@@ -19,7 +19,8 @@ Sources (the web pages these functions restate; short names used below):
 
 Group-wise scales and zero points (grouped.py) follow the W4A16 page's
 section 1 dequant form and the W8A16 page's extensions; NVFP4-style two-level
-block scaling (nvfp4.py) the W4A16 page's section 3.
+block scaling (nvfp4.py) the W4A16 page's section 3.  The paged key-value cache
+(kvcache.py) is written from its formulas.
 
 Parity status of each function is stated in its module.  Parity unpinned:
 the FP8 per-tensor scale formula (the FP8 page fixes only the 448 range and
@@ -49,6 +50,7 @@ from .grouped import (
     gemm_w4a16_grouped,
     gemm_w8a16_grouped,
 )
+from .kvcache import kv_plan, kv_append, paged_attention
 from .gemm import (
     dequant_w4,
     dequant_w8,
@@ -91,4 +93,7 @@ __all__ = [
     "NVFP4_BLOCK",
     "dequant_nvfp4",
     "gemm_nvfp4",
+    "kv_plan",
+    "kv_append",
+    "paged_attention",
 ]

@@ -584,7 +584,7 @@ def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scal
         raise ValueError(f"table and lens must have {batch} rows, one per request")
     width = table.shape[1]
     if max_len is None:
-        max_len = min(width * page_size, 2 ** 31 - 1)
+        max_len = min(width * page_size, 2 ** 30 - 1)
     need = qgemm_paged_attention_workspace_bytes(batch, heads, kv_heads, dim, max_len, window)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)

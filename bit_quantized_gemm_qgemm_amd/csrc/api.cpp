@@ -625,8 +625,8 @@ int64_t qgemm_paged_attention_workspace_bytes(int64_t batch, int64_t heads, int6
                                               int64_t dim, int64_t max_len, int64_t window) {
   if (!below(batch, 0, kMaxIndex) || !below(heads, 0, kMaxIndex) ||
       !below(kv_heads, 1, kMaxIndex) || heads % kv_heads != 0 || !kv_dim_ok(dim) ||
-      !below(max_len, 0, kMaxIndex) || !below(window, 0, kMaxIndex) ||
-      batch * heads >= kMaxIndex)
+      !below(max_len, 0, kMaxIndex / 2) || !below(window, 0, kMaxIndex) ||
+      batch * heads >= kMaxIndex || batch * qgemm::cdiv(max_len, 32) >= kMaxIndex)
     return QGEMM_ERR_SHAPE;
   return qgemm::paged_attention_workspace(batch, heads, kv_heads, dim, max_len, window);
 }
@@ -680,6 +680,7 @@ int qgemm_paged_attention(int dtype, int cache_dtype, const void* q, const void*
   a.kv_heads = (int)kv_heads;
   a.dim = (int)dim;
   a.pool = pool;
+  a.max_len = max_len;
   a.limit = max_len < width * page_size ? max_len : width * page_size;
   if (pages == 0) a.limit = 0;   // every page is missing
   a.window = window;

@@ -1,114 +1,619 @@
 // Attention of one new token per request over the paged key-value cache.
+//
+// For one request and one kv head, the heads that share it (up to 16 of them)
+// are the columns of two matrix products over a tile of 32 tokens:
+//   S^T [32 tokens x 16 heads] = K [32 x D] Q^T [D x 16]
+//   O^T [D x 16 heads]        += V^T [D x 32] P^T [32 x 16],  P = exp2(S - m)
+// with the running maximum m and sum l of each head kept per lane column.
+// The K index of a matrix instruction may be permuted freely as long as both
+// operands agree, and both uses of that make the kernel free of LDS and of
+// shuffles on the data path:
+//   - the 4 tokens that a lane holds of each S^T tile are the ones that it
+//     feeds as P^T: the token order of O^T's product is chosen as the order
+//     that S^T's accumulators come in;
+//   - V is read by rows (a lane takes W consecutive elements of 8 tokens) and
+//     transposed inside the lane by byte permutes, so that instruction j of
+//     the W makes the outputs d = W m + j.
+// The work is 4 D (K and V bytes) against 4 D group flops per token: bound by
+// the cache's bytes for every group.  What matters is bytes in flight: each
+// wave keeps one 32-token tile of K and V loading while it works on the last.
+#include <algorithm>
+
 #include "qgemm_common.h"
 
 namespace qgemm {
 namespace {
 
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
 constexpr int kAttnWaves = 4;
+constexpr int kTileTokens = 32;
+constexpr int kMaxGroup = 16;           // heads of one item: the columns of a matrix tile
 constexpr float kLog2e = 1.4426950408889634f;
 
+struct AttnArgs {
+  PagedAttention a;
+  uint32_t page_magic, page_shift;   // token / page_size = umulhi(2 token, magic) >> shift
+  int group;                         // heads of an item (its last chunk may hold fewer)
+  int chunks;                        // items per kv head
+  int groups;                        // workgroups that share the tiles; 0: one item each
+  int slot_floats;                   // of a partial result
+  int32_t* tiles_before;             // [batch + 1] in the workspace
+  float* partial;
+};
+
+// What a partial result holds: m[16], l[16], then o[heads][dim].
+constexpr int kSlotHead = 2 * kMaxGroup;
+
+template <int DT, bool E4M3, int KS>
+struct Attn {
+  static constexpr int W = KS <= 2 ? 4 : KS <= 4 ? 8 : 16;   // elements of V per lane and token
+  static constexpr int KD = E4M3 ? 2 : 4;                    // dwords of 8 elements of K
+  static constexpr int VD = W * (E4M3 ? 1 : 2) / 4;          // dwords of W elements of V
+  static constexpr int ES = E4M3 ? 1 : 2;
+  // probabilities and V enter the matrix cores as fp16 for e4m3 (its values
+  // are exact there and fp16 keeps more bits of P), else in the cache's type
+  static constexpr bool kHalfPV = E4M3 || DT == 1;
+  // fp16 probabilities are scaled by 2^15 so that the smallest ones stay
+  // normal; l carries the same factor
+  static constexpr float kBias = kHalfPV ? 15.0f : 0.0f;
+};
+
+// x of this lane and of the lane 16 (or 32) lanes away, as the two results of
+// exchanging rows between two copies of x.
+template <int DIST>
+__device__ __forceinline__ floatx2 both(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = DIST == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                            : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t y0 = y[0], y1 = y[1];
+  return floatx2{__builtin_bit_cast(float, y0), __builtin_bit_cast(float, y1)};
+}
+
+// over the four lanes 16 apart
+__device__ __forceinline__ float max_over_groups(float x) {
+  floatx2 y = both<16>(x);
+  y = both<32>(fmaxf(y[0], y[1]));
+  return fmaxf(y[0], y[1]);
+}
+
+__device__ __forceinline__ float sum_over_groups(float x) {
+  floatx2 y = both<16>(x);
+  y = both<32>(y[0] + y[1]);
+  return y[0] + y[1];
+}
+
+// Four e4m3 codes -> two dwords of 16-bit pairs (exact in fp16 and in bf16).
+template <bool HALF>
+__device__ __forceinline__ void expand_e4m3(uint32_t c, uint32_t* out) {
+  if constexpr (HALF) {
+    out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false));
+    out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, true));
+  } else {
+    out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+    out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+  }
+}
+
+template <bool HALF>
+__device__ __forceinline__ floatx4 mma(uintx4 a, uintx4 b, floatx4 c) {
+  if constexpr (HALF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                 __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// N dwords from p (16-byte pieces, or one 8- or 4-byte piece)
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t* r, const uint8_t* p) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uintx4 v = *reinterpret_cast<const uintx4*>(p + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[4 * i + j] = v[j];
+    }
+  } else if constexpr (N == 2) {
+    const uintx2 v = *reinterpret_cast<const uintx2*>(p);
+    r[0] = v[0];
+    r[1] = v[1];
+  } else {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
 template <int DT>
-__device__ __forceinline__ float to_float(uint16_t bits) {
-  if constexpr (DT == 1) return (float)__builtin_bit_cast(_Float16, bits);
-  return __builtin_bit_cast(float, (uint32_t)bits << 16);
+__device__ __forceinline__ uint16_t to_bits(float y) {
+  return DT == 1 ? f32_to_f16_bits(y) : f32_to_bf16_rne(y);
 }
 
-// e4m3fn code -> its value: the seven low bits read as an fp16 (bias 15
-// instead of 7) are value * 2^-8, subnormals included
-__device__ __forceinline__ float e4m3_value(uint8_t code) {
-  const uint32_t m = code & 0x7fu;
-  if (m == 0x7fu) return __builtin_nanf("");
-  const float v = (float)__builtin_bit_cast(_Float16, (uint16_t)(m << 7)) * 256.0f;
-  return code & 0x80u ? -v : v;
+// The tokens of request b that count: [first, n).
+__device__ __forceinline__ void token_range(const PagedAttention& a, int b, int* first, int* n) {
+  int len = a.lens[b];
+  len = len < 0 ? 0 : (len < a.limit ? len : (int)a.limit);
+  *n = len;
+  *first = a.window > 0 && len > a.window ? len - (int)a.window : 0;
 }
 
-template <int DT, bool E4M3>
-__device__ __forceinline__ float cache_value(const void* cache, int64_t i) {
-  if constexpr (E4M3) return e4m3_value(static_cast<const uint8_t*>(cache)[i]);
-  return to_float<DT>(static_cast<const uint16_t*>(cache)[i]);
+__device__ __forceinline__ int tiles_of(const PagedAttention& a, int b) {
+  int first, n;
+  token_range(a, b, &first, &n);
+  return (n - first + kTileTokens - 1) / kTileTokens;
 }
 
-// One workgroup per (head, request); its waves take tokens in turn, a lane
-// holding the elements lane + 64 j of the row.  Each wave keeps the running
-// maximum m, the sum l of exp(s - m) and the weighted sum of the values; the
-// waves are joined through LDS at the end.
-template <int DT, bool E4M3>
-__global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(const PagedAttention a) {
-  __shared__ float sm[kAttnWaves], sl[kAttnWaves], so[kAttnWaves][256];
+struct AttnShared {
+  float m[kAttnWaves][kMaxGroup], l[kAttnWaves][kMaxGroup];
+  int64_t scan[kAttnWaves];
+  int64_t total, before;
+  int request;
+};
+
+// Tokens [t0, t1) of one item (request b, heads h0 .. h0 + hn - 1, which share
+// kv head kvh) through the waves of the workgroup; the joined result goes to
+// `out` (divided and scaled) or, unscaled, to `slot`.
+template <int DT, bool E4M3, int KS>
+__device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, float* so, int b,
+                                       int kvh, int h0, int hn, int t0, int t1, float* slot) {
+  using A = Attn<DT, E4M3, KS>;
+  constexpr int W = A::W, KD = A::KD, VD = A::VD;
+  constexpr bool kHalfPV = A::kHalfPV;
+  const PagedAttention& a = args.a;
   const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
-  const int head = (int)blockIdx.x, b = (int)blockIdx.y;
-  const int kvh = head / (a.heads / a.kv_heads);
-  int64_t n = a.lens[b];
-  n = n < 0 ? 0 : (n < a.limit ? n : a.limit);
-  const int64_t first = a.window > 0 && n > a.window ? n - a.window : 0;
+  const int r = lane & 15, g = lane >> 4;
+  const int D = a.dim;
+
+  // Q^T: lane (head r, group g) holds elements 32 s + 8 g + [0, 8)
+  uintx4 qf[KS];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_batch_stride +
+                        (int64_t)(h0 + (r < hn ? r : 0)) * a.q_head_stride;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      qf[s] = uintx4{0, 0, 0, 0};
+      if (r < hn && 32 * s + 8 * g < D)
+        qf[s] = *reinterpret_cast<const uintx4*>(q + 32 * s + 8 * g);
+    }
+  }
   const float kscale = (E4M3 ? a.k_scale[kvh] : 1.0f) * a.scale * kLog2e;
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_batch_stride +
-                      head * a.q_head_stride;
-  float qv[4], o[4] = {0.f, 0.f, 0.f, 0.f};
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  const int head_row = kvh * a.pool.head_rows;
+  const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
+  // lanes past the row's end read its last elements (never stored)
+  const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache) + (W * r < D ? W * r : D - W) * A::ES;
+  const uint32_t row_bytes = (uint32_t)D * A::ES;
+
+  floatx4 acc[W];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) qv[j] = lane + 64 * j < a.dim ? to_float<DT>(q[lane + 64 * j]) : 0.f;
+  for (int j = 0; j < W; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
-  for (int64_t t = first + wave; t < n; t += kAttnWaves) {
-    const int64_t pi = t / a.pool.page_size, off = t - pi * a.pool.page_size;
-    const int32_t page = a.table[b * a.table_stride + pi];
-    if (page < 0 || page >= a.pool.pages) continue;
-    const int64_t row = (int64_t)page * a.pool.page_rows + (int64_t)kvh * a.pool.head_rows +
-                        off * a.pool.token_rows;
-    float s = 0.f;
+
+  constexpr int kStep = kTileTokens * kAttnWaves;
+  // Table entry of token t + (lane & 31); past the end, of the last token.
+  auto entry = [&](int t) {
+    t += lane & 31;
+    t = t < t1 ? t : t1 - 1;
+    return table[__umulhi(2u * (uint32_t)t, args.page_magic) >> args.page_shift];
+  };
+  // Its row, or -1 where the token does not count.
+  auto row = [&](int t, int32_t e) {
+    t += lane & 31;
+    const int page = (int)(__umulhi(2u * (uint32_t)t, args.page_magic) >> args.page_shift);
+    const int off = t - page * a.pool.page_size;
+    const bool ok = t < t1 && e >= 0 && e < a.pool.pages;
+    return ok ? e * a.pool.page_rows + head_row + off * a.pool.token_rows : -1;
+  };
+  uint32_t kr[2][KS][KD], vr[8][VD];
+  // Tokens that do not count read row 0 of the pool (there is one: a pool
+  // without pages has no tokens); what they read is dropped.
+  auto load_k = [&](int rows) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 64 * j < a.dim)
-        s += qv[j] * cache_value<DT, E4M3>(a.k_cache, row * a.dim + lane + 64 * j);
+    for (int u = 0; u < 2; ++u) {
+      const int x = __shfl(rows, 16 * u + r, 64);
+      const uint8_t* p = kc + (uint64_t)(uint32_t)(x < 0 ? 0 : x) * row_bytes;
 #pragma unroll
-    for (int x = 32; x > 0; x >>= 1) s += __shfl_xor(s, x, 64);
-    s *= kscale;
-    const float top = fmaxf(m, s);
+      for (int s = 0; s < KS; ++s) {
+        const int d = 32 * s + 8 * g;
+        load_dwords<KD>(kr[u][s], p + (d < D ? d : D - 8) * A::ES);
+      }
+    }
+  };
+  auto load_v = [&](int rows) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = __shfl(rows, 16 * (i >> 2) + 4 * g + (i & 3), 64);
+      load_dwords<VD>(vr[i], vc + (uint64_t)(uint32_t)(x < 0 ? 0 : x) * row_bytes);
+    }
+  };
+
+  int t = t0 + kTileTokens * wave;
+  if (t < t1) {
+    int32_t next_entry = entry(t + kStep);
+    int rows = row(t, entry(t));
+    load_k(rows);
+    load_v(rows);
+    for (; t < t1; t += kStep) {
+      const int32_t far_entry = entry(t + 2 * kStep);
+      const int next_rows = row(t + kStep, next_entry);
+      const bool whole = __all(rows >= 0);
+
+      // S^T
+      floatx4 sc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t kx[4];
+          if constexpr (E4M3) {
+            expand_e4m3<DT == 1>(kr[u][s][0], kx);
+            expand_e4m3<DT == 1>(kr[u][s][1], kx + 2);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kx[j] = kr[u][s][j];
+          }
+          if (32 * (s + 1) > D) {   // elements past the row's end
+            const bool in = 32 * s + 8 * g < D;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kx[j] = in ? kx[j] : 0u;
+          }
+          sc[u] = mma<DT == 1>(uintx4{kx[0], kx[1], kx[2], kx[3]}, qf[s], sc[u]);
+        }
+      }
+      load_k(next_rows);
+
+      // softmax over the tile: lane (head r, group g) has tokens 4 g + i of both halves
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = sc[i >> 2][i & 3] * kscale;
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool ok = __shfl(rows, 16 * (i >> 2) + 4 * g + (i & 3), 64) >= 0;
+          p[i] = ok ? p[i] : -INFINITY;
+#pragma unroll
+          for (int j = 0; j < VD; ++j) vr[i][j] = ok ? vr[i][j] : 0u;
+        }
+      }
+      float top = p[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
+      top = fmaxf(m, max_over_groups(top));
+      const float base = top == -INFINITY ? 0.f : top;
+      if (__any(top != m)) {
+        const float shrink = __builtin_amdgcn_exp2f(m - base);
+        l *= shrink;
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] *= shrink;
+        m = top;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(p[i] - base + A::kBias);
+        l += p[i];
+      }
+      // P^T in two 16-bit parts, both truncated, the second never 0: an
+      // infinite value of V times it has to stay infinite
+      uintx4 hi, lo;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kHalfPV) {
+          const auto h = __builtin_amdgcn_cvt_pkrtz(p[2 * i], p[2 * i + 1]);
+          hi[i] = __builtin_bit_cast(uint32_t, h);
+          lo[i] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_pkrtz(fmaxf(p[2 * i] - (float)h[0], 0x1p-24f),
+                                                   fmaxf(p[2 * i + 1] - (float)h[1], 0x1p-24f)));
+        } else {
+          const uint32_t x = __builtin_bit_cast(uint32_t, p[2 * i]);
+          const uint32_t y = __builtin_bit_cast(uint32_t, p[2 * i + 1]);
+          hi[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+          const float fx = p[2 * i] - __builtin_bit_cast(float, x & 0xffff0000u);
+          const float fy = p[2 * i + 1] - __builtin_bit_cast(float, y & 0xffff0000u);
+          lo[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, fmaxf(fy, 0x1p-100f)),
+                                        __builtin_bit_cast(uint32_t, fmaxf(fx, 0x1p-100f)),
+                                        0x07060302u);
+        }
+      }
+      // O^T: two elements (one dword of V's 16-bit values) of 8 tokens at a time
+#pragma unroll
+      for (int j4 = 0; j4 < W / 4; ++j4) {
+        uint32_t vx[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (E4M3) {
+            expand_e4m3<true>(vr[i][j4], vx[i]);
+          } else {
+            vx[i][0] = vr[i][2 * j4];
+            vx[i][1] = vr[i][2 * j4 + 1];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+          uintx4 vf;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            vf[i] = __builtin_amdgcn_perm(vx[2 * i + 1][j >> 1], vx[2 * i][j >> 1], sel);
+          acc[4 * j4 + j] = mma<kHalfPV>(vf, hi, acc[4 * j4 + j]);
+          acc[4 * j4 + j] = mma<kHalfPV>(vf, lo, acc[4 * j4 + j]);
+        }
+      }
+      load_v(next_rows);
+      rows = next_rows;
+      next_entry = far_entry;
+    }
+  }
+  l = sum_over_groups(l);
+
+  // Join the waves: sh.m, sh.l and so [wave][head][dim]
+  const int pitch = D + 4;
+  if (g == 0) {
+    sh.m[wave][r] = m;
+    sh.l[wave][r] = l;
+  }
+  if (r < hn) {
+    float* o = so + (wave * args.group + r) * pitch;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (W * (4 * g + i) < D) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[W * (4 * g + i) + j] = acc[j][i];
+      }
+  }
+  __syncthreads();
+  for (int x = (int)threadIdx.x; x < hn * D; x += 64 * kAttnWaves) {
+    const int h = x / D, d = x - h * D;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sh.m[w][h]);
     const float base = top == -INFINITY ? 0.f : top;
-    const float shrink = exp2f(m - base), p = exp2f(s - base);
-    m = top;
-    l = l * shrink + p;
+    float sum = 0.f, o = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 64 * j < a.dim)
-        o[j] = o[j] * shrink + p * cache_value<DT, E4M3>(a.v_cache, row * a.dim + lane + 64 * j);
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sh.m[w][h] - base);
+      sum += f * sh.l[w][h];
+      o += f * so[(w * args.group + h) * pitch + d];
+    }
+    if (slot) {
+      if (d == 0) {
+        slot[h] = top;
+        slot[kMaxGroup + h] = sum;
+      }
+      slot[kSlotHead + h * D + d] = o;
+    } else {
+      const float y = sum == 0.f ? 0.f : o / sum * (E4M3 ? a.v_scale[kvh] : 1.0f);
+      static_cast<uint16_t*>(a.out)[((int64_t)b * a.heads + h0 + h) * D + d] = to_bits<DT>(y);
+    }
   }
-  if (lane == 0) {
-    sm[wave] = m;
-    sl[wave] = l;
+  __syncthreads();
+}
+
+// Item i of a request: kv head i / chunks, heads from chunk i % chunks on.
+__device__ __forceinline__ void item_heads(const AttnArgs& args, int i, int* kvh, int* h0,
+                                           int* hn) {
+  const int per = args.a.heads / args.a.kv_heads;
+  *kvh = i / args.chunks;
+  const int c = (i - *kvh * args.chunks) * args.group;
+  *h0 = *kvh * per + c;
+  *hn = per - c < args.group ? per - c : args.group;
+}
+
+template <int DT, bool E4M3, int KS>
+__global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(const AttnArgs args) {
+  __shared__ float so[kAttnWaves * kMaxGroup * (32 * KS + 4)];
+  __shared__ AttnShared sh;
+  const PagedAttention& a = args.a;
+  const int items = a.kv_heads * args.chunks;
+  int kvh, h0, hn;
+  if (args.groups == 0) {   // one item per workgroup
+    const int b = (int)blockIdx.x / items;
+    item_heads(args, (int)blockIdx.x - b * items, &kvh, &h0, &hn);
+    int first, n;
+    token_range(a, b, &first, &n);
+    attend<DT, E4M3, KS>(args, sh, so, b, kvh, h0, hn, first, n, nullptr);
+    return;
   }
+  // The tiles of all items in one row, request by request, item by item:
+  // workgroup w takes its equal share of them, whatever the lengths are.
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kThreads = 64 * kAttnWaves;
+  int64_t start = 0, end = 0;
+  int b = 0;
+  int64_t before = 0;   // tiles of the requests before b, over one item
+  for (int pass = 0; pass < 2; ++pass) {   // the total, then the request that holds the start
+    int64_t sum = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      const int x = b0 + tid;
+      const int mine = x < a.batch ? tiles_of(a, x) : 0;
+      int64_t inc = mine;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) so[wave][lane + 64 * j] = o[j];
+      for (int off = 1; off < 64; off <<= 1) {
+        const int64_t y = __shfl_up(inc, off, 64);
+        if (lane >= off) inc += y;
+      }
+      if (lane == 63) sh.scan[wave] = inc;
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) inc += sh.scan[w];
+      if (pass == 0) {
+        if (blockIdx.x == 0 && x < a.batch) args.tiles_before[x + 1] = (int32_t)(sum + inc);
+      } else if (x < a.batch && items * (sum + inc - mine) <= start && start < items * (sum + inc)) {
+        sh.request = x;
+        sh.before = sum + inc - mine;
+      }
+      if (tid == kThreads - 1) sh.total = sum + inc;
+      __syncthreads();
+      sum = sh.total;
+    }
+    if (pass == 0) {
+      const int64_t total = items * sum;
+      if (blockIdx.x == 0 && tid == 0) args.tiles_before[0] = 0;
+      const int64_t used = total < args.groups ? total : args.groups;
+      if (blockIdx.x < used) {
+        start = blockIdx.x * total / used;
+        end = (blockIdx.x + 1) * total / used;
+      }
+    } else if (start < end) {
+      b = sh.request;
+      before = sh.before;
+    }
+  }
+  for (int64_t pos = start; pos < end;) {
+    const int tiles = tiles_of(a, b);
+    const int64_t at = pos - before * items;   // within the request
+    if (at >= (int64_t)tiles * items) {
+      before += tiles;
+      ++b;
+      continue;
+    }
+    const int i = (int)(at / tiles), tile0 = (int)(at - (int64_t)i * tiles);
+    const int64_t left = end - pos;
+    const int tile1 = tiles - tile0 < left ? tiles : tile0 + (int)left;
+    item_heads(args, i, &kvh, &h0, &hn);
+    int first, n;
+    token_range(a, b, &first, &n);
+    const int t1 = first + tile1 * kTileTokens;
+    // a part of an item goes to this workgroup's slot: 1 where it begins the
+    // item, else 0 (a share holds at most one of each)
+    float* slot = tile0 == 0 && tile1 == tiles
+                      ? nullptr
+                      : args.partial + (2 * (int64_t)blockIdx.x + (tile0 == 0)) * args.slot_floats;
+    attend<DT, E4M3, KS>(args, sh, so, b, kvh, h0, hn, first + tile0 * kTileTokens,
+                         t1 < n ? t1 : n, slot);
+    pos += tile1 - tile0;
+  }
+}
+
+// Joins the parts of the items that several workgroups shared, and writes the
+// zeros of requests without tokens.  One workgroup per (head, request).
+template <int DT>
+__global__ __launch_bounds__(256) void paged_attention_join_kernel(const AttnArgs args,
+                                                                   const float* v_scale) {
+  __shared__ float sums[4][256 + 4], weights[4];
+  const PagedAttention& a = args.a;
+  const int b = (int)(blockIdx.x / a.heads), head = (int)blockIdx.x - b * a.heads, D = a.dim;
+  const int items = a.kv_heads * args.chunks;
+  const int per = a.heads / a.kv_heads, kvh = head / per, in_kv = head - kvh * per;
+  const int i = kvh * args.chunks + in_kv / args.group, h = in_kv % args.group;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + ((int64_t)b * a.heads + head) * D;
+  const int64_t from = args.tiles_before[b], tiles = args.tiles_before[b + 1] - from;
+  if (tiles == 0) {
+    for (int d = (int)threadIdx.x; d < D; d += 256) out[d] = 0;
+    return;
+  }
+  const int64_t total = (int64_t)items * args.tiles_before[a.batch];
+  const int64_t used = total < args.groups ? total : args.groups;
+  const int64_t s = from * items + i * tiles, e = s + tiles;
+  const int w0 = (int)(((s + 1) * used - 1) / total), w1 = (int)((e * used - 1) / total);
+  if (w0 == w1) return;   // one workgroup had all of it
+  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  auto slot = [&](int w) {
+    return args.partial + (2 * (int64_t)w + (w == w0)) * args.slot_floats;
+  };
+  float top = -INFINITY;
+  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, slot(w)[h]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  const float base = top == -INFINITY ? 0.f : top;
+  // each wave takes every fourth part, a lane four of its elements
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+  for (int w = w0 + wave; w <= w1; w += 4) {
+    const float* x = slot(w);
+    const float f = __builtin_amdgcn_exp2f(x[h] - base);
+    sum += f * x[kMaxGroup + h];
+    if (4 * lane < D) {
+      const floatx4 v = *reinterpret_cast<const floatx4*>(x + kSlotHead + h * D + 4 * lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] += f * v[j];
+    }
+  }
+  if (lane == 0) weights[wave] = sum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sums[wave][4 * lane + j] = o[j];
   __syncthreads();
   const int d = (int)threadIdx.x;
-  if (d >= a.dim) return;
-  float top = -INFINITY;
-  for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm[w]);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc = 0.f;
-  for (int w = 0; w < kAttnWaves; ++w) {
-    const float f = exp2f(sm[w] - base);
-    sum += f * sl[w];
-    acc += f * so[w][d];
-  }
-  const float y = sum == 0.f ? 0.f : acc / sum * (E4M3 ? a.v_scale[kvh] : 1.0f);
-  static_cast<uint16_t*>(a.out)[((int64_t)b * a.heads + head) * a.dim + d] =
-      DT == 1 ? f32_to_f16_bits(y) : f32_to_bf16_rne(y);
+  if (d >= D) return;
+  sum = weights[0] + weights[1] + weights[2] + weights[3];
+  const float y = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+  out[d] = to_bits<DT>(sum == 0.f ? 0.f : y / sum * (v_scale ? v_scale[kvh] : 1.0f));
+}
+
+// ---- host side ---------------------------------------------------------------
+
+constexpr int kGroups = 512;          // two workgroups on each CU
+constexpr int64_t kOneItemTokens = 512;
+
+struct Shares {
+  int group, chunks, groups;
+  int64_t slot_floats;
+};
+
+Shares shares(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dim, int64_t max_len,
+              int64_t window) {
+  Shares s{};
+  const int64_t per = heads / kv_heads;
+  s.chunks = (int)cdiv(per, kMaxGroup);
+  s.group = s.chunks > 0 ? (int)cdiv(per, s.chunks) : 1;
+  s.slot_floats = kSlotHead + s.group * dim;
+  const int64_t span = window > 0 && window < max_len ? window : max_len;
+  if (span > kOneItemTokens) s.groups = kGroups;
+  (void)batch;
+  return s;
+}
+
+template <int DT, bool E4M3>
+hipError_t launch_ks(const AttnArgs& args, dim3 grid, hipStream_t stream) {
+  const int steps = (int)cdiv(args.a.dim, 32);
+  auto kernel = steps <= 2   ? paged_attention_kernel<DT, E4M3, 2>
+                : steps <= 3 ? paged_attention_kernel<DT, E4M3, 3>
+                : steps <= 4 ? paged_attention_kernel<DT, E4M3, 4>
+                : steps <= 6 ? paged_attention_kernel<DT, E4M3, 6>
+                             : paged_attention_kernel<DT, E4M3, 8>;
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * kAttnWaves), 0, stream, args);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t paged_attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
-  return 0;
+int64_t paged_attention_workspace(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dim,
+                                  int64_t max_len, int64_t window) {
+  if (batch == 0 || heads == 0) return 0;
+  const Shares s = shares(batch, heads, kv_heads, dim, max_len, window);
+  if (s.groups == 0) return 0;
+  return cdiv(4 * (batch + 1), 16) * 16 + 2 * s.groups * s.slot_floats * 4;
 }
 
 hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttention& a,
                                   hipStream_t stream) {
-  const dim3 grid((unsigned)a.heads, (unsigned)a.batch), block(64 * kAttnWaves);
+  AttnArgs args{};
+  args.a = a;
+  const Shares s = shares(a.batch, a.heads, a.kv_heads, a.dim, a.max_len, a.window);
+  args.group = s.group;
+  args.chunks = s.chunks;
+  args.groups = s.groups;
+  args.slot_floats = (int)s.slot_floats;
+  args.tiles_before = static_cast<int32_t*>(a.workspace);
+  args.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                          cdiv(4 * ((int64_t)a.batch + 1), 16) * 16);
+  // 2^(s-1) < P <= 2^s: ceil(2^(31+s) / P) fits 32 bits, and n * it >> (31 + s) is n / P for
+  // every n < 2^31 (the excess over n / P stays below 1 / P)
+  uint32_t shift = 0;
+  while (((uint64_t)1 << shift) < (uint64_t)a.pool.page_size) ++shift;
+  args.page_shift = shift;
+  args.page_magic = (uint32_t)((((uint64_t)1 << (31 + shift)) + a.pool.page_size - 1) /
+                               a.pool.page_size);
+  const dim3 grid(s.groups > 0 ? (unsigned)s.groups
+                               : (unsigned)((int64_t)a.batch * a.kv_heads * s.chunks));
   const bool e4m3 = cache_dtype == 3;
-  auto kernel =
-      dtype == 1 ? (e4m3 ? paged_attention_kernel<1, true> : paged_attention_kernel<1, false>)
-                 : (e4m3 ? paged_attention_kernel<2, true> : paged_attention_kernel<2, false>);
-  hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
+  hipError_t e =
+      dtype == 1 ? (e4m3 ? launch_ks<1, true>(args, grid, stream)
+                         : launch_ks<1, false>(args, grid, stream))
+                 : (e4m3 ? launch_ks<2, true>(args, grid, stream)
+                         : launch_ks<2, false>(args, grid, stream));
+  if (e != hipSuccess || s.groups == 0) return e;
+  const dim3 heads((unsigned)((int64_t)a.batch * a.heads));
+  auto join = dtype == 1 ? paged_attention_join_kernel<1> : paged_attention_join_kernel<2>;
+  hipLaunchKernelGGL(join, heads, dim3(256), 0, stream, args, e4m3 ? a.v_scale : nullptr);
   return hipGetLastError();
 }
 

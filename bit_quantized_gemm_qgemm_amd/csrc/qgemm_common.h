@@ -243,6 +243,7 @@ struct PagedAttention {
   int64_t q_batch_stride, q_head_stride, table_stride;
   int batch, heads, kv_heads, dim;
   KvPool pool;
+  int64_t max_len;
   int64_t limit;     // min(max_len, width * page_size)
   int64_t window;    // 0: none
   float scale;

@@ -399,8 +399,8 @@ int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
  * dense; cache_dtype is dtype or QGEMM_E4M3 (then k_scale, v_scale are fp32
  * [kv_heads], else NULL).  Products, softmax and sums are fp32 (the
  * probabilities enter the matrix cores as the sum of two 16-bit parts), the
- * output is rounded once.  max_len is a host-side bound of lens, which sizes
- * the launch.
+ * output is rounded once.  max_len is a host-side bound of lens below
+ * 2^30, which sizes the launch (batch * max_len / 32 below 2^31).
  *
  * workspace: qgemm_paged_attention_workspace_bytes(...) bytes, 16-byte
  * aligned, of any contents; calls that share one must not overlap.  May be

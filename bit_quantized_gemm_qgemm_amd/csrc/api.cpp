@@ -297,7 +297,7 @@ int check_kv_pool(int64_t kv_heads, int64_t dim, int64_t pages, int64_t page_siz
                   qgemm::KvPool* pool) {
   if (!kv_dim_ok(dim)) return QGEMM_ERR_SHAPE;
   if (!below(kv_heads, 0, kMaxIndex) || !below(pages, 0, kMaxIndex) ||
-      !below(page_size, 1, kMaxIndex))
+      !below(page_size, 1, kMaxIndex) || pages * page_size >= kMaxIndex)
     return QGEMM_ERR_SHAPE;
   for (int64_t st : {page_stride, head_stride, token_stride})
     if (!below(st, 0, kMaxIndex * dim) || st % dim != 0) return QGEMM_ERR_SHAPE;
@@ -590,7 +590,7 @@ int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
   if ((st = check_kv_pool(kv_heads, dim, pages, page_size, page_stride, head_stride, token_stride,
                           &pool)) != QGEMM_OK)
     return st;
-  if (!below(tokens, 0, kMaxIndex) || !kv_view_ok(k_token_stride, k_head_stride) ||
+  if (!below(tokens, 0, kMaxIndex) || tokens * kv_heads >= kMaxIndex || !kv_view_ok(k_token_stride, k_head_stride) ||
       !kv_view_ok(v_token_stride, v_head_stride))
     return QGEMM_ERR_SHAPE;
   const bool some = tokens > 0 && kv_heads > 0;

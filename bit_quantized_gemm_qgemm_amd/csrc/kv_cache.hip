@@ -17,7 +17,14 @@ namespace {
 // page's first position writes the table entry, and every thread takes the
 // number of a new page from the free list itself: nothing is read that this
 // launch writes.
+//
+// Several workgroups share the tokens in equal slices.  Each forms the sums
+// itself (8 bytes a request, from L2) up to the end of its slice, so none
+// waits for another; the first also writes them out, and the last one's slice
+// is open so that a device sum past the host's count still gets its pages.
 constexpr int kPlanThreads = 256;
+constexpr int kPlanSlice = 1024;       // tokens per workgroup, four a thread
+constexpr int kPlanGroups = 256;       // workgroups at most, one a CU
 
 struct PlanTile {
   int64_t tok[kPlanThreads + 1];    // tokens of the requests before, within all
@@ -27,12 +34,15 @@ struct PlanTile {
   int64_t wave[2][kPlanThreads / kWave];
 };
 
-__global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p) {
+__global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p, int64_t slice) {
   __shared__ PlanTile s;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t capacity = p.width * p.page_size;
+  const uint32_t P = (uint32_t)p.page_size;
+  const bool first = blockIdx.x == 0, last = blockIdx.x == gridDim.x - 1;
+  const int64_t from = blockIdx.x * slice, to = last ? INT64_MAX : from + slice;
   int64_t tok0 = 0, page0 = 0;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+  for (int64_t b0 = 0; b0 < p.batch && (first || tok0 < to); b0 += kPlanThreads) {
     const int64_t b = b0 + tid;
     int64_t cached = 0, added = 0, have = 0, take = 0;
     if (b < p.batch) {
@@ -43,7 +53,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p) {
       have = have < p.width ? have : p.width;
       take = cdiv(len, p.page_size) - have;
       take = take > 0 ? take : 0;
-      p.lens[b] = (int32_t)len;
+      if (first) p.lens[b] = (int32_t)len;
     }
     int64_t tok = added, page = take;   // inclusive sums over the wave, then the tile
 #pragma unroll
@@ -68,26 +78,27 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p) {
     s.cached[tid] = (int)cached;
     s.have[tid] = (int)have;
     if (tid == 0) s.tok[0] = tok0;
-    if (b < p.batch) {
+    if (first && b < p.batch) {
       p.cu_tokens[b] = (int32_t)(tok0 + tok - added);
       p.cu_pages[b] = (int32_t)(page0 + page - take);
     }
     if (tid == kPlanThreads - 1) s.wave[1][0] = page;   // the tile's pages, read after the barrier
     __syncthreads();
     const int64_t tile_pages = s.wave[1][0], tok_end = s.tok[kPlanThreads];
-    for (int64_t t = tok0 + tid; t < tok_end; t += kPlanThreads) {
+    const int64_t t1 = tok_end < to ? tok_end : to;
+    for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < t1; t += kPlanThreads) {
       int lo = 0, hi = kPlanThreads;   // the last request whose first token is not past t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s.tok[mid] <= t) lo = mid; else hi = mid;
       }
-      const int64_t pos = s.cached[lo] + (t - s.tok[lo]);
+      const int64_t pos = s.cached[lo] + (t - s.tok[lo]);   // below 2^32
       int64_t slot = -1;
       if (pos < capacity) {
-        const int64_t pi = pos / p.page_size, off = pos - pi * p.page_size;
+        const uint32_t pi = (uint32_t)pos / P, off = (uint32_t)pos - pi * P;
         int32_t* entry = p.table + (b0 + lo) * p.table_stride + pi;
         int32_t page_no;
-        if (pi < s.have[lo]) {
+        if (pi < (uint32_t)s.have[lo]) {
           page_no = *entry;
         } else {
           const int64_t f = s.page[lo] + pi - s.have[lo];
@@ -102,11 +113,13 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p) {
     page0 += tile_pages;
     __syncthreads();   // the tile is rewritten next
   }
-  if (tid == 0) {
+  if (first && tid == 0) {
     p.cu_tokens[p.batch] = (int32_t)tok0;
     p.cu_pages[p.batch] = (int32_t)page0;
   }
-  for (int64_t t = tok0 + tid; t < p.tokens; t += kPlanThreads) p.slots[t] = -1;
+  // slots past the last token (the sums are complete where this runs at all)
+  const int64_t end = to < p.tokens ? to : p.tokens;
+  for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < end; t += kPlanThreads) p.slots[t] = -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -129,54 +142,65 @@ __device__ __forceinline__ float to_float(uint16_t bits) {
   return __builtin_bit_cast(float, (uint32_t)bits << 16);
 }
 
-// One thread per 8 elements of one row (token, kv head), for keys
-// (blockIdx.y = 0) and values (1).
+// A thread moves 8 elements of one row (token, kv head), of the keys and of
+// the values: the row's number, its slot and its place in the pool are found
+// once for both, and two 16-byte loads are in flight.
 template <int DT, bool E4M3>
-__global__ __launch_bounds__(256) void kv_append_kernel(const KvAppend a) {
-  const int part = (int)blockIdx.y;
+__global__ __launch_bounds__(256) void kv_append_kernel(const KvAppend a, int rows_per_group) {
   const int chunks = a.dim / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.tokens * a.kv_heads * chunks) return;
-  const int c = (int)(i % chunks);
-  const int h = (int)(i / chunks % a.kv_heads);
-  const int64_t t = i / chunks / a.kv_heads;
+  const int local = (int)threadIdx.x / chunks, c = (int)threadIdx.x - local * chunks;
+  const int64_t rows = a.tokens * a.kv_heads;   // below 2^31
+  const int64_t n = (int64_t)blockIdx.x * rows_per_group + local;
+  if (local >= rows_per_group || n >= rows) return;
+  const uint32_t t = (uint32_t)n / (uint32_t)a.kv_heads;
+  const int h = (int)((uint32_t)n - t * (uint32_t)a.kv_heads);
+  uintx4 v[2];
+#pragma unroll
+  for (int part = 0; part < 2; ++part)
+    v[part] = *reinterpret_cast<const uintx4*>(static_cast<const uint16_t*>(a.x[part]) +
+                                               t * a.token_stride[part] +
+                                               h * a.head_stride[part] + 8 * c);
   const int64_t slot = a.slots[t];
   if (slot < 0 || slot >= (int64_t)a.pool.pages * a.pool.page_size) return;
-  const int64_t page = slot / a.pool.page_size, off = slot - page * a.pool.page_size;
-  const int64_t row = page * a.pool.page_rows + (int64_t)h * a.pool.head_rows +
-                      off * a.pool.token_rows;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x[part]) + t * a.token_stride[part] +
-                      h * a.head_stride[part] + 8 * c;
-  const uintx4 v = *reinterpret_cast<const uintx4*>(x);
-  if constexpr (!E4M3) {
-    uint16_t* y = static_cast<uint16_t*>(a.cache[part]) + row * a.dim + 8 * c;
-    *reinterpret_cast<uintx4*>(y) = v;
-  } else {
-    const float scale = a.scale[part][h];
-    uintx2 w = {0, 0};
+  const uint32_t page = (uint32_t)slot / (uint32_t)a.pool.page_size;
+  const uint32_t off = (uint32_t)slot - page * (uint32_t)a.pool.page_size;
+  const int64_t at = (int64_t)(page * (uint32_t)a.pool.page_rows +
+                               (uint32_t)h * (uint32_t)a.pool.head_rows +
+                               off * (uint32_t)a.pool.token_rows) * a.dim + 8 * c;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float f = to_float<DT>((uint16_t)(v[j >> 1] >> (16 * (j & 1))));
-      w[j >> 2] |= e4m3_code(f / scale) << (8 * (j & 3));
+  for (int part = 0; part < 2; ++part) {
+    if constexpr (!E4M3) {
+      *reinterpret_cast<uintx4*>(static_cast<uint16_t*>(a.cache[part]) + at) = v[part];
+    } else {
+      const float scale = a.scale[part][h];
+      uintx2 w = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = to_float<DT>((uint16_t)(v[part][j >> 1] >> (16 * (j & 1))));
+        w[j >> 2] |= e4m3_code(f / scale) << (8 * (j & 3));
+      }
+      *reinterpret_cast<uintx2*>(static_cast<uint8_t*>(a.cache[part]) + at) = w;
     }
-    uint8_t* y = static_cast<uint8_t*>(a.cache[part]) + row * a.dim + 8 * c;
-    *reinterpret_cast<uintx2*>(y) = w;
   }
 }
 
 }  // namespace
 
 hipError_t launch_kv_plan(const KvPlan& p, hipStream_t stream) {
-  hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+  int64_t groups = cdiv(p.tokens, kPlanSlice);
+  groups = groups < 1 ? 1 : groups < kPlanGroups ? groups : kPlanGroups;
+  hipLaunchKernelGGL(kv_plan_kernel, dim3((unsigned)groups), dim3(kPlanThreads), 0, stream, p,
+                     cdiv(p.tokens, groups));
   return hipGetLastError();
 }
 
 hipError_t launch_kv_append(int dtype, int cache_dtype, const KvAppend& a, hipStream_t stream) {
-  const dim3 grid((unsigned)cdiv(a.tokens * a.kv_heads * (a.dim / 8), 256), 2), block(256);
+  const int rows = 256 / (a.dim / 8);   // whole rows of a workgroup
+  const dim3 grid((unsigned)cdiv(a.tokens * a.kv_heads, rows)), block(256);
   const bool e4m3 = cache_dtype == 3;
   auto kernel = dtype == 1 ? (e4m3 ? kv_append_kernel<1, true> : kv_append_kernel<1, false>)
                            : (e4m3 ? kv_append_kernel<2, true> : kv_append_kernel<2, false>);
-  hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
+  hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, rows);
   return hipGetLastError();
 }
 

@@ -334,7 +334,8 @@ int qgemm_w8a16_grouped(const void* x, const void* w_packed, void* y, int64_t M,
  * arrays 8-byte alignment only; q, k and v may be strided views (strides in
  * elements, multiples of 8), for instance the three parts of a fused QKV
  * product.  dim is a multiple of 16 up to 256.  The pools may be of any size
- * in bytes, with fewer than 2^31 rows of dim elements.
+ * in bytes, with fewer than 2^31 slots and rows of dim elements; an append
+ * takes fewer than 2^31 rows.
  */
 enum qgemm_dtype {
   QGEMM_F16 = 1,

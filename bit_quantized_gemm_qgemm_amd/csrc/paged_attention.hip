@@ -46,10 +46,13 @@ struct AttnArgs {
 // What a partial result holds: m[16], l[16], then o[heads][dim].
 constexpr int kSlotHead = 2 * kMaxGroup;
 
-template <int DT, bool E4M3, int KS>
+template <int DT, bool E4M3, int KS, bool FULL>
 struct Attn {
   static constexpr int W = KS <= 2 ? 4 : KS <= 4 ? 8 : 16;   // elements of V per lane and token
-  static constexpr int KD = E4M3 ? 2 : 4;                    // dwords of 8 elements of K
+  // K: a lane takes 16 bytes of a row at a time, 4 lanes 64 bytes of it: the
+  // elements of one step of 32, or of two steps for e4m3
+  static constexpr int KE = E4M3 ? 16 : 8;
+  static constexpr int KL = KS * 8 / KE;                     // loads per row
   static constexpr int VD = W * (E4M3 ? 1 : 2) / 4;          // dwords of W elements of V
   static constexpr int ES = E4M3 ? 1 : 2;
   // probabilities and V enter the matrix cores as fp16 for e4m3 (its values
@@ -57,6 +60,7 @@ struct Attn {
   static constexpr bool kHalfPV = E4M3 || DT == 1;
   // fp16 probabilities are scaled by 2^15 so that the smallest ones stay
   // normal; l carries the same factor
+  static constexpr int kResident = KS > 4 ? 2 : KS > 2 ? 3 : 4;
   static constexpr float kBias = kHalfPV ? 15.0f : 0.0f;
 };
 
@@ -84,6 +88,14 @@ __device__ __forceinline__ float sum_over_groups(float x) {
   return y[0] + y[1];
 }
 
+// x of lane I of this lane's 16
+template <int I>
+__device__ __forceinline__ uint64_t in_group(uint64_t x) {
+  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)x, 0x150 + I, 0xf, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(x >> 32), 0x150 + I, 0xf, 0xf, false);
+  return (uint64_t)hi << 32 | lo;
+}
+
 // Four e4m3 codes -> two dwords of 16-bit pairs (exact in fp16 and in bf16).
 template <bool HALF>
 __device__ __forceinline__ void expand_e4m3(uint32_t c, uint32_t* out) {
@@ -105,22 +117,25 @@ __device__ __forceinline__ floatx4 mma(uintx4 a, uintx4 b, floatx4 c) {
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// N dwords from p (16-byte pieces, or one 8- or 4-byte piece)
+// N dwords from p (16-byte pieces, or one 8- or 4-byte piece).  Non-temporal,
+// like the loads of K: each byte of the cache is used once, and kept out of
+// the caches it leaves them to what is read again (128K tokens, bf16: 97 ->
+// 80 us).
 template <int N>
 __device__ __forceinline__ void load_dwords(uint32_t* r, const uint8_t* p) {
   if constexpr (N >= 4) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uintx4 v = *reinterpret_cast<const uintx4*>(p + 16 * i);
+      const uintx4 v = __builtin_nontemporal_load(reinterpret_cast<const uintx4*>(p + 16 * i));
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[4 * i + j] = v[j];
     }
   } else if constexpr (N == 2) {
-    const uintx2 v = *reinterpret_cast<const uintx2*>(p);
+    const uintx2 v = __builtin_nontemporal_load(reinterpret_cast<const uintx2*>(p));
     r[0] = v[0];
     r[1] = v[1];
   } else {
-    r[0] = *reinterpret_cast<const uint32_t*>(p);
+    r[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
   }
 }
 
@@ -146,36 +161,24 @@ __device__ __forceinline__ int tiles_of(const PagedAttention& a, int b) {
 struct AttnShared {
   float m[kAttnWaves][kMaxGroup], l[kAttnWaves][kMaxGroup];
   int64_t scan[kAttnWaves];
-  int64_t total, before;
+  int64_t before;
   int request;
 };
 
 // Tokens [t0, t1) of one item (request b, heads h0 .. h0 + hn - 1, which share
 // kv head kvh) through the waves of the workgroup; the joined result goes to
 // `out` (divided and scaled) or, unscaled, to `slot`.
-template <int DT, bool E4M3, int KS>
-__device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, float* so, int b,
+template <int DT, bool E4M3, int KS, bool FULL>
+__device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uintx4* sq, float* so, int b,
                                        int kvh, int h0, int hn, int t0, int t1, float* slot) {
-  using A = Attn<DT, E4M3, KS>;
-  constexpr int W = A::W, KD = A::KD, VD = A::VD;
+  using A = Attn<DT, E4M3, KS, FULL>;
+  constexpr int W = A::W, KE = A::KE, KL = A::KL, VD = A::VD;
   constexpr bool kHalfPV = A::kHalfPV;
   const PagedAttention& a = args.a;
   const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int D = a.dim;
 
-  // Q^T: lane (head r, group g) holds elements 32 s + 8 g + [0, 8)
-  uintx4 qf[KS];
-  {
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_batch_stride +
-                        (int64_t)(h0 + (r < hn ? r : 0)) * a.q_head_stride;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      qf[s] = uintx4{0, 0, 0, 0};
-      if (r < hn && 32 * s + 8 * g < D)
-        qf[s] = *reinterpret_cast<const uintx4*>(q + 32 * s + 8 * g);
-    }
-  }
   const float kscale = (E4M3 ? a.k_scale[kvh] : 1.0f) * a.scale * kLog2e;
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
   const int head_row = kvh * a.pool.head_rows;
@@ -190,158 +193,202 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, flo
   float m = -INFINITY, l = 0.f;
 
   constexpr int kStep = kTileTokens * kAttnWaves;
-  // Table entry of token t + (lane & 31); past the end, of the last token.
+  // A lane looks up one token of a tile (lanes r >= 8 repeat): the one whose V
+  // row the whole group g takes as its r-th, so that row goes round the group
+  // by a broadcast within its 16 lanes.
+  const int my_token = 16 * ((r >> 2) & 1) + 4 * g + (r & 3);
+  // Table entry of that token; past the end, of the last one.
   auto entry = [&](int t) {
-    t += lane & 31;
+    t += my_token;
     t = t < t1 ? t : t1 - 1;
     return table[__umulhi(2u * (uint32_t)t, args.page_magic) >> args.page_shift];
   };
   // Its row, or -1 where the token does not count.
   auto row = [&](int t, int32_t e) {
-    t += lane & 31;
+    t += my_token;
     const int page = (int)(__umulhi(2u * (uint32_t)t, args.page_magic) >> args.page_shift);
     const int off = t - page * a.pool.page_size;
     const bool ok = t < t1 && e >= 0 && e < a.pool.pages;
     return ok ? e * a.pool.page_rows + head_row + off * a.pool.token_rows : -1;
   };
-  uint32_t kr[2][KS][KD], vr[8][VD];
+  // lanes that looked up tokens r and 16 + r
+  const int k_lane = 16 * (r >> 2) + (r & 3);
+  uintx4 kr[2][KL];
+  uint32_t vr[8][VD];
   // Tokens that do not count read row 0 of the pool (there is one: a pool
   // without pages has no tokens); what they read is dropped.
-  auto load_k = [&](int rows) {
+  auto load_k = [&](const int (&x)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int x = __shfl(rows, 16 * u + r, 64);
-      const uint8_t* p = kc + (uint64_t)(uint32_t)(x < 0 ? 0 : x) * row_bytes;
+      const uint8_t* p = kc + (uint64_t)(uint32_t)x[u] * row_bytes;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int d = 32 * s + 8 * g;
-        load_dwords<KD>(kr[u][s], p + (d < D ? d : D - 8) * A::ES);
+      for (int s = 0; s < KL; ++s) {
+        const int d = KE * (4 * s + g);
+        kr[u][s] = __builtin_nontemporal_load(
+            reinterpret_cast<const uintx4*>(p + (FULL || d < D ? d : D - KE) * A::ES));
       }
     }
   };
   auto load_v = [&](int rows) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int x = __shfl(rows, 16 * (i >> 2) + 4 * g + (i & 3), 64);
-      load_dwords<VD>(vr[i], vc + (uint64_t)(uint32_t)(x < 0 ? 0 : x) * row_bytes);
-    }
+    const uint64_t at = (uint64_t)(uint32_t)(rows < 0 ? 0 : rows) * row_bytes;
+    load_dwords<VD>(vr[0], vc + in_group<0>(at));
+    load_dwords<VD>(vr[1], vc + in_group<1>(at));
+    load_dwords<VD>(vr[2], vc + in_group<2>(at));
+    load_dwords<VD>(vr[3], vc + in_group<3>(at));
+    load_dwords<VD>(vr[4], vc + in_group<4>(at));
+    load_dwords<VD>(vr[5], vc + in_group<5>(at));
+    load_dwords<VD>(vr[6], vc + in_group<6>(at));
+    load_dwords<VD>(vr[7], vc + in_group<7>(at));
+  };
+  auto k_rows = [&](int rows, int (&x)[2]) {
+    rows = rows < 0 ? 0 : rows;
+    x[0] = __shfl(rows, k_lane, 64);
+    x[1] = __shfl(rows, k_lane + 4, 64);
   };
 
+  // Q^T goes to LDS as the lanes of a wave read it: lane (head r, group g) takes the
+  // elements of each step that it takes of K.  Read again for every tile: 4 KS
+  // registers less.  Wave w brings steps w, w + 4, ...; loaded first, stored
+  // once the wave's first tile is on its way.
+  constexpr int kQSteps = (KS + kAttnWaves - 1) / kAttnWaves;
+  uintx4 qx[kQSteps];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_batch_stride +
+                        (int64_t)(h0 + (r < hn ? r : 0)) * a.q_head_stride;
+#pragma unroll
+    for (int x = 0; x < kQSteps; ++x) {
+      const int s = wave + kAttnWaves * x;
+      const int d = E4M3 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+      qx[x] = uintx4{0, 0, 0, 0};
+      if (r < hn && s < KS && (FULL || d < D)) qx[x] = *reinterpret_cast<const uintx4*>(q + d);
+    }
+  }
   int t = t0 + kTileTokens * wave;
+  int32_t next_entry = 0;
+  int rows = -1, kx_rows[2];
   if (t < t1) {
-    int32_t next_entry = entry(t + kStep);
-    int rows = row(t, entry(t));
-    load_k(rows);
+    next_entry = entry(t + kStep);
+    rows = row(t, entry(t));
+    k_rows(rows, kx_rows);
+    load_k(kx_rows);
+    // K before V here as in the loop: the loop's wait for K then leaves V in flight
+    asm volatile("" ::: "memory");
     load_v(rows);
-    for (; t < t1; t += kStep) {
-      const int32_t far_entry = entry(t + 2 * kStep);
-      const int next_rows = row(t + kStep, next_entry);
-      const bool whole = __all(rows >= 0);
+  }
+#pragma unroll
+  for (int x = 0; x < kQSteps; ++x)
+    if (wave + kAttnWaves * x < KS) sq[64 * (wave + kAttnWaves * x) + lane] = qx[x];
+  __syncthreads();
+  for (; t < t1; t += kStep) {
+    asm volatile("" ::: "memory");   // Q stays in LDS: not hoisted out of the loop
+    const int32_t far_entry = entry(t + 2 * kStep);
+    const int next_rows = row(t + kStep, next_entry);
+    k_rows(next_rows, kx_rows);
+    const uint64_t counts = __ballot(rows >= 0);
 
-      // S^T
-      floatx4 sc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    // S^T
+    floatx4 sc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
+    for (int s = 0; s < KS; ++s) {
+      const uintx4 qf = sq[64 * s + lane];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t kx[4];
-          if constexpr (E4M3) {
-            expand_e4m3<DT == 1>(kr[u][s][0], kx);
-            expand_e4m3<DT == 1>(kr[u][s][1], kx + 2);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) kx[j] = kr[u][s][j];
-          }
-          if (32 * (s + 1) > D) {   // elements past the row's end
-            const bool in = 32 * s + 8 * g < D;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) kx[j] = in ? kx[j] : 0u;
-          }
-          sc[u] = mma<DT == 1>(uintx4{kx[0], kx[1], kx[2], kx[3]}, qf[s], sc[u]);
+      for (int u = 0; u < 2; ++u) {
+        uintx4 kx = kr[u][s * 8 / KE];
+        // the row's end falls into the last two steps
+        if (!FULL && s >= KS - 2 && KE * (4 * (s * 8 / KE) + g) >= D) kx = uintx4{0, 0, 0, 0};
+        if constexpr (E4M3) {
+          uint32_t x[4];
+          expand_e4m3<DT == 1>(kx[2 * (s & 1)], x);
+          expand_e4m3<DT == 1>(kx[2 * (s & 1) + 1], x + 2);
+          kx = uintx4{x[0], x[1], x[2], x[3]};
         }
+        sc[u] = mma<DT == 1>(kx, qf, sc[u]);
       }
-      load_k(next_rows);
+    }
+    load_k(kx_rows);
 
-      // softmax over the tile: lane (head r, group g) has tokens 4 g + i of both halves
-      float p[8];
+    // softmax over the tile: lane (head r, group g) has tokens 4 g + i of both halves
+    float p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = sc[i >> 2][i & 3] * kscale;
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool ok = __shfl(rows, 16 * (i >> 2) + 4 * g + (i & 3), 64) >= 0;
-          p[i] = ok ? p[i] : -INFINITY;
-#pragma unroll
-          for (int j = 0; j < VD; ++j) vr[i][j] = ok ? vr[i][j] : 0u;
-        }
-      }
-      float top = p[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
-      top = fmaxf(m, max_over_groups(top));
-      const float base = top == -INFINITY ? 0.f : top;
-      if (__any(top != m)) {
-        const float shrink = __builtin_amdgcn_exp2f(m - base);
-        l *= shrink;
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] *= shrink;
-        m = top;
-      }
+    for (int i = 0; i < 8; ++i) p[i] = sc[i >> 2][i & 3] * kscale;
+    if (counts != ~0ull) {
+      asm volatile("");   // a branch, not selects: V is waited for here only
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(p[i] - base + A::kBias);
-        l += p[i];
+        const bool ok = (counts >> (16 * g + i)) & 1;   // of the lane that looked it up
+        p[i] = ok ? p[i] : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VD; ++j) vr[i][j] = ok ? vr[i][j] : 0u;
       }
-      // P^T in two 16-bit parts, both truncated, the second never 0: an
-      // infinite value of V times it has to stay infinite
-      uintx4 hi, lo;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (kHalfPV) {
-          const auto h = __builtin_amdgcn_cvt_pkrtz(p[2 * i], p[2 * i + 1]);
-          hi[i] = __builtin_bit_cast(uint32_t, h);
-          lo[i] = __builtin_bit_cast(
-              uint32_t, __builtin_amdgcn_cvt_pkrtz(fmaxf(p[2 * i] - (float)h[0], 0x1p-24f),
-                                                   fmaxf(p[2 * i + 1] - (float)h[1], 0x1p-24f)));
-        } else {
-          const uint32_t x = __builtin_bit_cast(uint32_t, p[2 * i]);
-          const uint32_t y = __builtin_bit_cast(uint32_t, p[2 * i + 1]);
-          hi[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-          const float fx = p[2 * i] - __builtin_bit_cast(float, x & 0xffff0000u);
-          const float fy = p[2 * i + 1] - __builtin_bit_cast(float, y & 0xffff0000u);
-          lo[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, fmaxf(fy, 0x1p-100f)),
-                                        __builtin_bit_cast(uint32_t, fmaxf(fx, 0x1p-100f)),
-                                        0x07060302u);
-        }
-      }
-      // O^T: two elements (one dword of V's 16-bit values) of 8 tokens at a time
-#pragma unroll
-      for (int j4 = 0; j4 < W / 4; ++j4) {
-        uint32_t vx[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (E4M3) {
-            expand_e4m3<true>(vr[i][j4], vx[i]);
-          } else {
-            vx[i][0] = vr[i][2 * j4];
-            vx[i][1] = vr[i][2 * j4 + 1];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
-          uintx4 vf;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            vf[i] = __builtin_amdgcn_perm(vx[2 * i + 1][j >> 1], vx[2 * i][j >> 1], sel);
-          acc[4 * j4 + j] = mma<kHalfPV>(vf, hi, acc[4 * j4 + j]);
-          acc[4 * j4 + j] = mma<kHalfPV>(vf, lo, acc[4 * j4 + j]);
-        }
-      }
-      load_v(next_rows);
-      rows = next_rows;
-      next_entry = far_entry;
     }
+    float top = p[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
+    // m is the maximum rounded up to a whole number: the factor 2^15, the
+    // difference of two m and the shrinking by it are exact, and m moves less
+    top = fmaxf(m, __builtin_ceilf(max_over_groups(top)));
+    const float base = (top == -INFINITY ? 0.f : top) - A::kBias;
+    if (__any(top != m)) {
+      const float shrink = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
+      l *= shrink;
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j] *= shrink;
+      m = top;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(p[i] - base);
+      l += p[i];
+    }
+    // P^T in two 16-bit parts, both truncated, the second never 0: an
+    // infinite value of V times it has to stay infinite
+    uintx4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kHalfPV) {
+        const auto h = __builtin_amdgcn_cvt_pkrtz(p[2 * i], p[2 * i + 1]);
+        hi[i] = __builtin_bit_cast(uint32_t, h);
+        lo[i] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_pkrtz(fmaxf(p[2 * i] - (float)h[0], 0x1p-24f),
+                                                 fmaxf(p[2 * i + 1] - (float)h[1], 0x1p-24f)));
+      } else {
+        const uint32_t x = __builtin_bit_cast(uint32_t, p[2 * i]);
+        const uint32_t y = __builtin_bit_cast(uint32_t, p[2 * i + 1]);
+        hi[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        const float fx = p[2 * i] - __builtin_bit_cast(float, x & 0xffff0000u);
+        const float fy = p[2 * i + 1] - __builtin_bit_cast(float, y & 0xffff0000u);
+        lo[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, fmaxf(fy, 0x1p-100f)),
+                                      __builtin_bit_cast(uint32_t, fmaxf(fx, 0x1p-100f)),
+                                      0x07060302u);
+      }
+    }
+    // O^T: two elements (one dword of V's 16-bit values) of 8 tokens at a time
+#pragma unroll
+    for (int j4 = 0; j4 < W / 4; ++j4) {
+      uint32_t vx[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (E4M3) {
+          expand_e4m3<true>(vr[i][j4], vx[i]);
+        } else {
+          vx[i][0] = vr[i][2 * j4];
+          vx[i][1] = vr[i][2 * j4 + 1];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+        uintx4 vf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vf[i] = __builtin_amdgcn_perm(vx[2 * i + 1][j >> 1], vx[2 * i][j >> 1], sel);
+        acc[4 * j4 + j] = mma<kHalfPV>(vf, hi, acc[4 * j4 + j]);
+        acc[4 * j4 + j] = mma<kHalfPV>(vf, lo, acc[4 * j4 + j]);
+      }
+    }
+    load_v(next_rows);
+    rows = next_rows;
+    next_entry = far_entry;
   }
   l = sum_over_groups(l);
 
@@ -398,8 +445,10 @@ __device__ __forceinline__ void item_heads(const AttnArgs& args, int i, int* kvh
   *hn = per - c < args.group ? per - c : args.group;
 }
 
-template <int DT, bool E4M3, int KS>
-__global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(const AttnArgs args) {
+template <int DT, bool E4M3, int KS, bool FULL>
+__global__ __launch_bounds__(64 * kAttnWaves, (Attn<DT, E4M3, KS, FULL>::kResident))
+void paged_attention_kernel(const AttnArgs args) {
+  __shared__ uintx4 sq[64 * KS];
   __shared__ float so[kAttnWaves * kMaxGroup * (32 * KS + 4)];
   __shared__ AttnShared sh;
   const PagedAttention& a = args.a;
@@ -410,7 +459,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(const 
     item_heads(args, (int)blockIdx.x - b * items, &kvh, &h0, &hn);
     int first, n;
     token_range(a, b, &first, &n);
-    attend<DT, E4M3, KS>(args, sh, so, b, kvh, h0, hn, first, n, nullptr);
+    attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first, n, nullptr);
     return;
   }
   // The tiles of all items in one row, request by request, item by item:
@@ -420,42 +469,61 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(const 
   int64_t start = 0, end = 0;
   int b = 0;
   int64_t before = 0;   // tiles of the requests before b, over one item
-  for (int pass = 0; pass < 2; ++pass) {   // the total, then the request that holds the start
-    int64_t sum = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-      const int x = b0 + tid;
-      const int mine = x < a.batch ? tiles_of(a, x) : 0;
-      int64_t inc = mine;
+  int64_t sum = 0, inc = 0;
+  int mine = 0;
+  auto scan = [&](int b0) {   // the sum up to request b0 + tid, this one's included, in inc
+    const int x = b0 + tid;
+    mine = x < a.batch ? tiles_of(a, x) : 0;
+    inc = mine;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int64_t y = __shfl_up(inc, off, 64);
-        if (lane >= off) inc += y;
-      }
-      if (lane == 63) sh.scan[wave] = inc;
-      __syncthreads();
-      for (int w = 0; w < wave; ++w) inc += sh.scan[w];
-      if (pass == 0) {
-        if (blockIdx.x == 0 && x < a.batch) args.tiles_before[x + 1] = (int32_t)(sum + inc);
-      } else if (x < a.batch && items * (sum + inc - mine) <= start && start < items * (sum + inc)) {
-        sh.request = x;
-        sh.before = sum + inc - mine;
-      }
-      if (tid == kThreads - 1) sh.total = sum + inc;
-      __syncthreads();
-      sum = sh.total;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t y = __shfl_up(inc, off, 64);
+      if (lane >= off) inc += y;
     }
-    if (pass == 0) {
-      const int64_t total = items * sum;
-      if (blockIdx.x == 0 && tid == 0) args.tiles_before[0] = 0;
-      const int64_t used = total < args.groups ? total : args.groups;
-      if (blockIdx.x < used) {
-        start = blockIdx.x * total / used;
-        end = (blockIdx.x + 1) * total / used;
-      }
-    } else if (start < end) {
-      b = sh.request;
-      before = sh.before;
+    if (lane == 63) sh.scan[wave] = inc;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const int64_t y = sh.scan[w];
+      if (w < wave) inc += y;
+      all += y;
     }
+    inc += sum;
+    sum += all;
+  };
+  auto find = [&](int b0) {   // the request that holds the start
+    if (start < end && items * (inc - mine) <= start && start < items * inc) {
+      sh.request = b0 + tid;
+      sh.before = inc - mine;
+    }
+    __syncthreads();   // also before sh.scan is written again
+  };
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    if (b0 > 0) __syncthreads();
+    scan(b0);
+    if (blockIdx.x == 0 && b0 + tid < a.batch) args.tiles_before[b0 + tid + 1] = (int32_t)inc;
+  }
+  if (blockIdx.x == 0 && tid == 0) args.tiles_before[0] = 0;
+  const int64_t total = items * sum;
+  const int64_t used = total < args.groups ? total : args.groups;
+  if (blockIdx.x < used) {
+    start = blockIdx.x * total / used;
+    end = (blockIdx.x + 1) * total / used;
+  }
+  if (a.batch <= kThreads) {   // the sums are still at hand
+    find(0);
+  } else {
+    sum = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      __syncthreads();
+      scan(b0);
+      find(b0);
+    }
+  }
+  if (start < end) {
+    b = sh.request;
+    before = sh.before;
   }
   for (int64_t pos = start; pos < end;) {
     const int tiles = tiles_of(a, b);
@@ -477,7 +545,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(const 
     float* slot = tile0 == 0 && tile1 == tiles
                       ? nullptr
                       : args.partial + (2 * (int64_t)blockIdx.x + (tile0 == 0)) * args.slot_floats;
-    attend<DT, E4M3, KS>(args, sh, so, b, kvh, h0, hn, first + tile0 * kTileTokens,
+    attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first + tile0 * kTileTokens,
                          t1 < n ? t1 : n, slot);
     pos += tile1 - tile0;
   }
@@ -540,7 +608,8 @@ __global__ __launch_bounds__(256) void paged_attention_join_kernel(const AttnArg
 
 // ---- host side ---------------------------------------------------------------
 
-constexpr int kGroups = 512;          // two workgroups on each CU
+constexpr int kCus = 256;
+constexpr int kMaxGroups = 4 * kCus;
 constexpr int64_t kOneItemTokens = 512;
 
 struct Shares {
@@ -556,21 +625,37 @@ Shares shares(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dim, int64
   s.group = s.chunks > 0 ? (int)cdiv(per, s.chunks) : 1;
   s.slot_floats = kSlotHead + s.group * dim;
   const int64_t span = window > 0 && window < max_len ? window : max_len;
-  if (span > kOneItemTokens) s.groups = kGroups;
+  if (span > kOneItemTokens) s.groups = kMaxGroups;
   (void)batch;
   return s;
 }
 
-template <int DT, bool E4M3>
-hipError_t launch_ks(const AttnArgs& args, dim3 grid, hipStream_t stream) {
-  const int steps = (int)cdiv(args.a.dim, 32);
-  auto kernel = steps <= 2   ? paged_attention_kernel<DT, E4M3, 2>
-                : steps <= 3 ? paged_attention_kernel<DT, E4M3, 3>
-                : steps <= 4 ? paged_attention_kernel<DT, E4M3, 4>
-                : steps <= 6 ? paged_attention_kernel<DT, E4M3, 6>
-                             : paged_attention_kernel<DT, E4M3, 8>;
-  hipLaunchKernelGGL(kernel, grid, dim3(64 * kAttnWaves), 0, stream, args);
+template <int DT, bool E4M3, int KS, bool FULL>
+hipError_t launch_main(AttnArgs* args, hipStream_t stream) {
+  if (args->groups > 0) args->groups = kCus * Attn<DT, E4M3, KS, FULL>::kResident;
+  const PagedAttention& a = args->a;
+  const dim3 grid(args->groups > 0 ? (unsigned)args->groups
+                                   : (unsigned)((int64_t)a.batch * a.kv_heads * args->chunks));
+  hipLaunchKernelGGL((paged_attention_kernel<DT, E4M3, KS, FULL>), grid, dim3(64 * kAttnWaves), 0, stream,
+                     *args);
   return hipGetLastError();
+}
+
+template <int DT, bool E4M3, int KS>
+hipError_t launch_full(AttnArgs* args, hipStream_t stream) {
+  return args->a.dim == 32 * KS ? launch_main<DT, E4M3, KS, true>(args, stream)
+                                : launch_main<DT, E4M3, KS, false>(args, stream);
+}
+
+template <int DT, bool E4M3>
+hipError_t launch_ks(AttnArgs* args, hipStream_t stream) {
+  const int steps = (int)cdiv(args->a.dim, 32);
+  if (steps <= 2) return launch_full<DT, E4M3, 2>(args, stream);
+  if constexpr (!E4M3)   // e4m3 takes its steps in twos
+    if (steps <= 3) return launch_full<DT, E4M3, 3>(args, stream);
+  if (steps <= 4) return launch_full<DT, E4M3, 4>(args, stream);
+  if (steps <= 6) return launch_full<DT, E4M3, 6>(args, stream);
+  return launch_full<DT, E4M3, 8>(args, stream);
 }
 
 }  // namespace
@@ -602,14 +687,11 @@ hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttenti
   args.page_shift = shift;
   args.page_magic = (uint32_t)((((uint64_t)1 << (31 + shift)) + a.pool.page_size - 1) /
                                a.pool.page_size);
-  const dim3 grid(s.groups > 0 ? (unsigned)s.groups
-                               : (unsigned)((int64_t)a.batch * a.kv_heads * s.chunks));
   const bool e4m3 = cache_dtype == 3;
-  hipError_t e =
-      dtype == 1 ? (e4m3 ? launch_ks<1, true>(args, grid, stream)
-                         : launch_ks<1, false>(args, grid, stream))
-                 : (e4m3 ? launch_ks<2, true>(args, grid, stream)
-                         : launch_ks<2, false>(args, grid, stream));
+  const hipError_t e = dtype == 1 ? (e4m3 ? launch_ks<1, true>(&args, stream)
+                                          : launch_ks<1, false>(&args, stream))
+                                  : (e4m3 ? launch_ks<2, true>(&args, stream)
+                                          : launch_ks<2, false>(&args, stream));
   if (e != hipSuccess || s.groups == 0) return e;
   const dim3 heads((unsigned)((int64_t)a.batch * a.heads));
   auto join = dtype == 1 ? paged_attention_join_kernel<1> : paged_attention_join_kernel<2>;

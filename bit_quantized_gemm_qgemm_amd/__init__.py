@@ -100,7 +100,10 @@ def _check(status, where):
 
 
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """Handle of torch's current stream on t's device (as
+    torch.cuda.current_stream gives it, without the Stream object: 0.1 us
+    instead of 1.9)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
@@ -429,15 +432,22 @@ def qgemm_fp8_act_noalloc(a, b_packed, scale_b, N, out):
 
 
 # ---- paged key-value cache ---------------------------------------------------
+#
+# These calls are made for every layer of every decode step and the kernels
+# behind them take a few microseconds, so their checks are kept to a few
+# attribute reads per tensor; _refuse says what is wrong once something is.
 
 # qgemm_dtype codes; uint8 holds e4m3fn codes, as qgemm_quantize_fp8 returns them
 _HALF_TYPES = {torch.float16: 1, torch.bfloat16: 2}
 _CACHE_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.uint8: 3}
+_INT32 = (torch.int32,)
+_INT64 = (torch.int64,)
+_FLOAT32 = (torch.float32,)
+_UINT8 = (torch.uint8,)
 
 
-def _view(t, dtypes, ndim, name):
-    """A device tensor of one of `dtypes` whose last axis is dense; the other
-    axes may have any strides."""
+def _refuse(t, dtypes, ndim, name, device, dense):
+    """Raise for a tensor that failed a check of _dense or _view."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
@@ -446,46 +456,58 @@ def _view(t, dtypes, ndim, name):
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel() > 0:
-        raise ValueError(f"the last axis of {name} must be dense")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on {device}")
+    raise ValueError(f"{name} must be contiguous (row-major, no padding)" if dense
+                     else f"the last axis of {name} must be dense")
 
 
-def _strides(t):
-    """Strides of all axes but the last; 0 where an axis has one entry or none,
-    whose stride torch leaves arbitrary."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride())]
+def _dense(t, dtypes, ndim, name, device):
+    """A contiguous tensor of one of `dtypes` on device number `device`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == ndim and t.is_cuda
+            and t.get_device() == device and t.is_contiguous()):
+        _refuse(t, dtypes, ndim, name, device, True)
 
 
-def _same_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+def _view(t, dtypes, ndim, name, device=None):
+    """A tensor of one of `dtypes` whose last axis is dense; the other axes may
+    have any strides.  Returns (shape, strides of all axes but the last): 0
+    where an axis has one entry or none, whose stride torch leaves arbitrary.
+    With no `device` number given the tensor sets it."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == ndim and t.is_cuda
+            and (device is None or t.get_device() == device)):
+        _refuse(t, dtypes, ndim, name, device, False)
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
+        _refuse(t, dtypes, ndim, name, t.get_device(), False)
+    if 1 in shape or 0 in shape:
+        return shape, [st if n > 1 else 0 for n, st in zip(shape[:-1], strides)]
+    return shape, strides[:-1]
 
 
-def _kv_pools(k_cache, v_cache, k_scale, v_scale, dtype):
+def _kv_pools(k_cache, v_cache, k_scale, v_scale, dtype, device):
     """Check both pools; returns (type code, [pages, kv_heads, page_size, dim],
-    strides of the first three axes)."""
-    _view(k_cache, _CACHE_TYPES, 4, "k_cache")
-    _view(v_cache, _CACHE_TYPES, 4, "v_cache")
-    shape, strides = k_cache.shape, _strides(k_cache)
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != shape or _strides(v_cache) != strides:
+    strides of the first three axes, addresses of the scales)."""
+    shape, strides = _view(k_cache, _CACHE_TYPES, 4, "k_cache", device)
+    v_shape, v_strides = _view(v_cache, _CACHE_TYPES, 4, "v_cache", device)
+    if v_cache.dtype != k_cache.dtype or v_shape != shape or v_strides != strides:
         raise ValueError("k_cache and v_cache must agree in type, shape and strides")
+    if shape[2] < 1:
+        raise ValueError("pages must hold at least one token")
     code = _CACHE_TYPES[k_cache.dtype]
     if code == 3:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is None:
                 raise ValueError(f"an e4m3 cache needs {name} (float32, one per kv head)")
-            _need(t, torch.float32, 1, name)
+            _dense(t, _FLOAT32, 1, name, device)
             if t.shape[0] != shape[1]:
                 raise ValueError(f"{name} must have {shape[1]} entries, one per kv head")
-    else:
-        if k_cache.dtype != dtype:
-            raise TypeError(f"a 16-bit cache must be {dtype} like the tokens, got {k_cache.dtype}")
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("a 16-bit cache takes no scales")
-    if shape[2] < 1:
-        raise ValueError("pages must hold at least one token")
-    return code, shape, strides
+        return code, shape, strides, k_scale.data_ptr(), v_scale.data_ptr()
+    if k_cache.dtype != dtype:
+        raise TypeError(f"a 16-bit cache must be {dtype} like the tokens, got {k_cache.dtype}")
+    if k_scale is not None or v_scale is not None:
+        raise ValueError("a 16-bit cache takes no scales")
+    return code, shape, strides, None, None
 
 
 def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None):
@@ -498,32 +520,38 @@ def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None)
     those four tensors to write into.  tokens: how many tokens the host counts
     on (the sum of added).  cu_pages[-1] is the number of pages taken; past
     the end of free_pages entries and slots become -1."""
-    _view(table, (torch.int32,), 2, "table")
-    batch, width = table.shape
-    for t, name in ((cached, "cached"), (added, "added")):
-        _need(t, torch.int32, 1, name)
-        if t.shape[0] != batch:
-            raise ValueError(f"{name} must have {batch} entries, one per request")
-    _need(free_pages, torch.int32, 1, "free_pages")
+    (batch, width), (table_stride,) = _view(table, _INT32, 2, "table")
+    device = table.get_device()
+    _dense(cached, _INT32, 1, "cached", device)
+    _dense(added, _INT32, 1, "added", device)
+    _dense(free_pages, _INT32, 1, "free_pages", device)
+    if cached.shape[0] != batch or added.shape[0] != batch:
+        raise ValueError(f"cached and added must have {batch} entries, one per request")
     if page_size < 1 or tokens < 0:
         raise ValueError("page_size must be at least 1 and tokens at least 0")
-    sizes = ((torch.int32, batch), (torch.int32, batch + 1), (torch.int32, batch + 1),
-             (torch.int64, tokens))
     if out is None:
-        out = tuple(torch.empty(n, dtype=d, device=table.device) for d, n in sizes)
+        i32 = {"dtype": torch.int32, "device": table.device}
+        out = (torch.empty(batch, **i32), torch.empty(batch + 1, **i32),
+               torch.empty(batch + 1, **i32),
+               torch.empty(tokens, dtype=torch.int64, device=table.device))
+        lens, cu_tokens, cu_pages, slots = out
     else:
         out = tuple(out)
         if len(out) != 4:
             raise ValueError("out must be (lens, cu_tokens, cu_pages, slots)")
-        for t, (d, n), name in zip(out, sizes, ("lens", "cu_tokens", "cu_pages", "slots")):
-            _need(t, d, 1, name)
-            if t.shape[0] != n:
-                raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    _same_device(table, cached, added, free_pages, *out)
-    _check(lib().qgemm_kv_plan(table.data_ptr(), cached.data_ptr(), added.data_ptr(),
-                               free_pages.data_ptr(), *(t.data_ptr() for t in out), batch, width,
-                               _strides(table)[0], free_pages.shape[0], page_size, tokens,
-                               _stream(table)), "qgemm_kv_plan")
+        lens, cu_tokens, cu_pages, slots = out
+        _dense(lens, _INT32, 1, "lens", device)
+        _dense(cu_tokens, _INT32, 1, "cu_tokens", device)
+        _dense(cu_pages, _INT32, 1, "cu_pages", device)
+        _dense(slots, _INT64, 1, "slots", device)
+        if (lens.shape[0] != batch or cu_tokens.shape[0] != batch + 1
+                or cu_pages.shape[0] != batch + 1 or slots.shape[0] != tokens):
+            raise ValueError(f"lens, cu_tokens, cu_pages and slots must have {batch}, {batch + 1}, "
+                             f"{batch + 1} and {tokens} entries")
+    _check(lib().qgemm_kv_plan(
+        table.data_ptr(), cached.data_ptr(), added.data_ptr(), free_pages.data_ptr(),
+        lens.data_ptr(), cu_tokens.data_ptr(), cu_pages.data_ptr(), slots.data_ptr(), batch, width,
+        table_stride, free_pages.shape[0], page_size, tokens, _stream(table)), "qgemm_kv_plan")
     return out
 
 
@@ -533,21 +561,20 @@ def qgemm_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     0: skipped) of the pools [pages, kv_heads, page_size, dim], in place.
     Pools of the same type take a copy; float8_e4m3fn (or uint8 code) pools
     take e4m3fn(x / scale[head]), k_scale and v_scale float32 [kv_heads]."""
-    _view(k, _HALF_TYPES, 3, "k")
-    _view(v, (k.dtype,), 3, "v")
-    _need(slots, torch.int64, 1, "slots")
-    code, (pages, kv_heads, page_size, dim), strides = _kv_pools(k_cache, v_cache, k_scale,
-                                                                v_scale, k.dtype)
+    shape, k_strides = _view(k, _HALF_TYPES, 3, "k")
+    device, dtype = k.get_device(), k.dtype
+    v_shape, v_strides = _view(v, (dtype,), 3, "v", device)
+    _dense(slots, _INT64, 1, "slots", device)
+    code, (pages, kv_heads, page_size, dim), strides, k_scale, v_scale = _kv_pools(
+        k_cache, v_cache, k_scale, v_scale, dtype, device)
     tokens = slots.shape[0]
-    if tuple(k.shape) != (tokens, kv_heads, dim) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [{tokens}, {kv_heads}, {dim}], got {list(k.shape)} "
-                         f"and {list(v.shape)}")
-    _same_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    if shape != (tokens, kv_heads, dim) or v_shape != shape:
+        raise ValueError(f"k and v must be [{tokens}, {kv_heads}, {dim}], got {list(shape)} "
+                         f"and {list(v_shape)}")
     _check(lib().qgemm_kv_append(
-        _HALF_TYPES[k.dtype], code, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if code == 3 else None,
-        v_scale.data_ptr() if code == 3 else None, tokens, kv_heads, dim, *_strides(k),
-        *_strides(v), pages, page_size, *strides, _stream(k)), "qgemm_kv_append")
+        _HALF_TYPES[dtype], code, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, tokens, kv_heads, dim,
+        *k_strides, *v_strides, pages, page_size, *strides, _stream(k)), "qgemm_kv_append")
 
 
 def qgemm_paged_attention_workspace_bytes(batch, heads, kv_heads, dim, max_len, window=0):
@@ -570,40 +597,38 @@ def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scal
     workspace: uint8, at least qgemm_paged_attention_workspace_bytes(batch,
     heads, kv_heads, dim, max_len, window); allocated if None.  Returns out,
     [batch, heads, dim] of q's type."""
-    _view(q, _HALF_TYPES, 3, "q")
-    code, (pages, kv_heads, page_size, dim), strides = _kv_pools(k_cache, v_cache, k_scale,
-                                                                v_scale, q.dtype)
-    batch, heads = q.shape[:2]
-    if q.shape[2] != dim:
-        raise ValueError(f"q has head size {q.shape[2]}, the cache {dim}")
+    shape, q_strides = _view(q, _HALF_TYPES, 3, "q")
+    device, dtype = q.get_device(), q.dtype
+    batch, heads, dim = shape
+    code, (pages, kv_heads, page_size, cache_dim), strides, k_scale, v_scale = _kv_pools(
+        k_cache, v_cache, k_scale, v_scale, dtype, device)
+    if dim != cache_dim:
+        raise ValueError(f"q has head size {dim}, the cache {cache_dim}")
     if kv_heads < 1 or heads % kv_heads:
         raise ValueError(f"{heads} heads do not divide over {kv_heads} kv heads")
-    _view(table, (torch.int32,), 2, "table")
-    _need(lens, torch.int32, 1, "lens")
-    if table.shape[0] != batch or lens.shape[0] != batch:
+    (rows, width), (table_stride,) = _view(table, _INT32, 2, "table", device)
+    _dense(lens, _INT32, 1, "lens", device)
+    if rows != batch or lens.shape[0] != batch:
         raise ValueError(f"table and lens must have {batch} rows, one per request")
-    width = table.shape[1]
     if max_len is None:
         max_len = min(width * page_size, 2 ** 30 - 1)
     need = qgemm_paged_attention_workspace_bytes(batch, heads, kv_heads, dim, max_len, window)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     else:
-        _need(workspace, torch.uint8, 1, "workspace")
+        _dense(workspace, _UINT8, 1, "workspace", device)
         if workspace.shape[0] < need:
             raise ValueError(f"workspace needs {need} bytes")
     if out is None:
-        out = torch.empty((batch, heads, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
     else:
-        _need(out, q.dtype, 3, "out")
-        if out.shape != q.shape:
-            raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-    _same_device(q, k_cache, v_cache, table, lens, k_scale, v_scale, workspace, out)
+        _dense(out, (dtype,), 3, "out", device)
+        if out.shape != shape:
+            raise ValueError(f"out must be {list(shape)}, got {list(out.shape)}")
     _check(lib().qgemm_paged_attention(
-        _HALF_TYPES[q.dtype], code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        table.data_ptr(), lens.data_ptr(), k_scale.data_ptr() if code == 3 else None,
-        v_scale.data_ptr() if code == 3 else None, out.data_ptr(), workspace.data_ptr(), batch,
-        heads, kv_heads, dim, *_strides(q), pages, page_size, *strides, width, _strides(table)[0],
+        _HALF_TYPES[dtype], code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        table.data_ptr(), lens.data_ptr(), k_scale, v_scale, out.data_ptr(), workspace.data_ptr(),
+        batch, heads, kv_heads, dim, *q_strides, pages, page_size, *strides, width, table_stride,
         max_len, window, dim ** -0.5 if scale is None else scale, _stream(q)),
         "qgemm_paged_attention")
     return out

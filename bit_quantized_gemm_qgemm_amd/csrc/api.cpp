@@ -590,8 +590,9 @@ int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
   if ((st = check_kv_pool(kv_heads, dim, pages, page_size, page_stride, head_stride, token_stride,
                           &pool)) != QGEMM_OK)
     return st;
-  if (!below(tokens, 0, kMaxIndex) || tokens * kv_heads >= kMaxIndex || !kv_view_ok(k_token_stride, k_head_stride) ||
-      !kv_view_ok(v_token_stride, v_head_stride))
+  // a thread takes 8 elements; a launch has fewer than 2^32 threads
+  if (!below(tokens, 0, kMaxIndex) || tokens * kv_heads >= kMaxIndex / (dim / 8) ||
+      !kv_view_ok(k_token_stride, k_head_stride) || !kv_view_ok(v_token_stride, v_head_stride))
     return QGEMM_ERR_SHAPE;
   const bool some = tokens > 0 && kv_heads > 0;
   if (!present(k, some) || !present(v, some) || !present(slots, tokens) ||
@@ -626,7 +627,7 @@ int64_t qgemm_paged_attention_workspace_bytes(int64_t batch, int64_t heads, int6
   if (!below(batch, 0, kMaxIndex) || !below(heads, 0, kMaxIndex) ||
       !below(kv_heads, 1, kMaxIndex) || heads % kv_heads != 0 || !kv_dim_ok(dim) ||
       !below(max_len, 0, kMaxIndex / 2) || !below(window, 0, kMaxIndex) ||
-      batch * heads >= kMaxIndex || batch * qgemm::cdiv(max_len, 32) >= kMaxIndex)
+      batch * heads >= kMaxIndex / 256 || batch * qgemm::cdiv(max_len, 32) >= kMaxIndex)
     return QGEMM_ERR_SHAPE;
   return qgemm::paged_attention_workspace(batch, heads, kv_heads, dim, max_len, window);
 }

@@ -39,8 +39,9 @@ struct AttnArgs {
   int chunks;                        // items per kv head
   int groups;                        // workgroups that share the tiles; 0: one item each
   int slot_floats;                   // of a partial result
-  int32_t* tiles_before;             // [batch + 1] in the workspace
-  float* partial;
+  // in the workspace, where workgroups share items
+  uint32_t* parts;                   // [batch * items]: first workgroup << 16 | further ones
+  float* partial;                    // two slots for each workgroup
 };
 
 // What a partial result holds: m[16], l[16], then o[heads][dim].
@@ -158,10 +159,35 @@ __device__ __forceinline__ int tiles_of(const PagedAttention& a, int b) {
   return (n - first + kTileTokens - 1) / kTileTokens;
 }
 
+// The tiles of all items stand in one row, request by request, item by item,
+// each item followed by kItemCost empty places: what it costs a workgroup to
+// take up one more (its first loads, the join of its waves), in tiles.
+// Workgroup w gets the w-th of `used` equal stretches of that row.  With 8
+// places against none: 64 requests of 256 to 8192 tokens, e4m3, 77 -> 68 us.
+constexpr int kItemCost = 8;
+constexpr int kMinShare = 2 * kAttnWaves;   // places; a tile for each wave and the item's cost
+
+__device__ __forceinline__ int places_of(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
+
+struct Stretches {
+  uint64_t size, longer;   // the first `longer` of them hold one place more
+  __device__ __forceinline__ Stretches(uint64_t total, uint64_t used) {
+    size = total / used;
+    longer = total - size * used;
+  }
+  __device__ __forceinline__ uint64_t start(uint64_t w) const {
+    return w * size + (w < longer ? w : longer);
+  }
+  __device__ __forceinline__ uint32_t holder(uint64_t place) const {
+    const uint64_t split = longer * (size + 1);
+    return (uint32_t)(place < split ? place / (size + 1) : longer + (place - split) / size);
+  }
+};
+
 struct AttnShared {
   float m[kAttnWaves][kMaxGroup], l[kAttnWaves][kMaxGroup];
-  int64_t scan[kAttnWaves];
-  int64_t before;
+  uint32_t scan[kAttnWaves];
+  uint32_t before;
   int request;
 };
 
@@ -462,30 +488,28 @@ void paged_attention_kernel(const AttnArgs args) {
     attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first, n, nullptr);
     return;
   }
-  // The tiles of all items in one row, request by request, item by item:
-  // workgroup w takes its equal share of them, whatever the lengths are.
+  // The places of all items (see Stretches), whatever the lengths are.
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kThreads = 64 * kAttnWaves;
-  int64_t start = 0, end = 0;
-  int b = 0;
-  int64_t before = 0;   // tiles of the requests before b, over one item
-  int64_t sum = 0, inc = 0;
-  int mine = 0;
+  // the requests without tokens among blockIdx.x, + gridDim.x, ... are this workgroup's
+  const bool empty = (int)blockIdx.x < a.batch && tiles_of(a, (int)blockIdx.x) == 0;
+  uint64_t start = 0, end = 0;
+  uint32_t sum = 0, inc = 0, mine = 0;   // places over one item: below 2^32 by the host's checks
   auto scan = [&](int b0) {   // the sum up to request b0 + tid, this one's included, in inc
     const int x = b0 + tid;
-    mine = x < a.batch ? tiles_of(a, x) : 0;
+    mine = x < a.batch ? places_of(tiles_of(a, x)) : 0;
     inc = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int64_t y = __shfl_up(inc, off, 64);
+      const uint32_t y = __shfl_up(inc, off, 64);
       if (lane >= off) inc += y;
     }
     if (lane == 63) sh.scan[wave] = inc;
     __syncthreads();
-    int64_t all = 0;
+    uint32_t all = 0;
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) {
-      const int64_t y = sh.scan[w];
+      const uint32_t y = sh.scan[w];
       if (w < wave) inc += y;
       all += y;
     }
@@ -493,7 +517,7 @@ void paged_attention_kernel(const AttnArgs args) {
     sum += all;
   };
   auto find = [&](int b0) {   // the request that holds the start
-    if (start < end && items * (inc - mine) <= start && start < items * inc) {
+    if (start < end && (uint64_t)items * (inc - mine) <= start && start < (uint64_t)items * inc) {
       sh.request = b0 + tid;
       sh.before = inc - mine;
     }
@@ -502,14 +526,14 @@ void paged_attention_kernel(const AttnArgs args) {
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     if (b0 > 0) __syncthreads();
     scan(b0);
-    if (blockIdx.x == 0 && b0 + tid < a.batch) args.tiles_before[b0 + tid + 1] = (int32_t)inc;
   }
-  if (blockIdx.x == 0 && tid == 0) args.tiles_before[0] = 0;
-  const int64_t total = items * sum;
-  const int64_t used = total < args.groups ? total : args.groups;
+  const uint64_t total = (uint64_t)items * sum;
+  uint64_t used = total / kMinShare;
+  used = used < 1 ? 1 : used < (uint64_t)args.groups ? used : args.groups;
+  const Stretches shares(total, used);
   if (blockIdx.x < used) {
-    start = blockIdx.x * total / used;
-    end = (blockIdx.x + 1) * total / used;
+    start = shares.start(blockIdx.x);
+    end = shares.start(blockIdx.x + 1);
   }
   if (a.batch <= kThreads) {   // the sums are still at hand
     find(0);
@@ -521,113 +545,158 @@ void paged_attention_kernel(const AttnArgs args) {
       find(b0);
     }
   }
+  int b = 0;
+  uint64_t before = 0;   // places of the requests before b
   if (start < end) {
     b = sh.request;
-    before = sh.before;
+    before = (uint64_t)items * sh.before;
   }
-  for (int64_t pos = start; pos < end;) {
-    const int tiles = tiles_of(a, b);
-    const int64_t at = pos - before * items;   // within the request
-    if (at >= (int64_t)tiles * items) {
-      before += tiles;
+  for (uint64_t pos = start; pos < end;) {
+    const int tiles = tiles_of(a, b), places = places_of(tiles);
+    const uint64_t at = pos - before;   // within the request
+    if (at >= (uint64_t)places * items) {
+      before += (uint64_t)places * items;
       ++b;
       continue;
     }
-    const int i = (int)(at / tiles), tile0 = (int)(at - (int64_t)i * tiles);
-    const int64_t left = end - pos;
-    const int tile1 = tiles - tile0 < left ? tiles : tile0 + (int)left;
-    item_heads(args, i, &kvh, &h0, &hn);
-    int first, n;
-    token_range(a, b, &first, &n);
-    const int t1 = first + tile1 * kTileTokens;
-    // a part of an item goes to this workgroup's slot: 1 where it begins the
-    // item, else 0 (a share holds at most one of each)
-    float* slot = tile0 == 0 && tile1 == tiles
-                      ? nullptr
-                      : args.partial + (2 * (int64_t)blockIdx.x + (tile0 == 0)) * args.slot_floats;
-    attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first + tile0 * kTileTokens,
-                         t1 < n ? t1 : n, slot);
-    pos += tile1 - tile0;
+    const int i = (int)(at / (uint32_t)places), tile0 = (int)(at - (uint64_t)i * places);
+    const uint64_t left = end - pos;
+    const int stop = (uint64_t)(places - tile0) < left ? places : tile0 + (int)left;
+    const int tile1 = stop < tiles ? stop : tiles;
+    if (tile0 < tile1) {
+      item_heads(args, i, &kvh, &h0, &hn);
+      int first, n;
+      token_range(a, b, &first, &n);
+      const int t1 = first + tile1 * kTileTokens;
+      // a part of an item goes to this workgroup's slot: 1 where it begins the
+      // item, else 0 (a stretch holds at most one of each)
+      float* slot = tile0 == 0 && tile1 == tiles
+                        ? nullptr
+                        : args.partial + (2 * (int64_t)blockIdx.x + (tile0 == 0)) * args.slot_floats;
+      if (tile0 == 0 && tid == 0) {
+        const uint32_t last = tile1 == tiles ? blockIdx.x : shares.holder(pos + tiles - 1);
+        args.parts[(int64_t)b * items + i] = blockIdx.x << 16 | (last - blockIdx.x);
+      }
+      attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first + tile0 * kTileTokens,
+                                 t1 < n ? t1 : n, slot);
+    }
+    pos += stop - tile0;
+  }
+  for (int x = (int)blockIdx.x; x < a.batch; x += (int)gridDim.x) {
+    if (x == (int)blockIdx.x ? !empty : tiles_of(a, x) != 0) continue;
+    uint32_t* out = static_cast<uint32_t*>(a.out) + (int64_t)x * a.heads * (a.dim / 2);
+    for (int j = tid; j < a.heads * (a.dim / 2); j += kThreads) out[j] = 0;
+    for (int j = tid; j < items; j += kThreads) args.parts[(int64_t)x * items + j] = 0;
   }
 }
 
-// Joins the parts of the items that several workgroups shared, and writes the
-// zeros of requests without tokens.  One workgroup per (head, request).
-template <int DT>
-__global__ __launch_bounds__(256) void paged_attention_join_kernel(const AttnArgs args,
-                                                                   const float* v_scale) {
-  __shared__ float sums[4][256 + 4], weights[4];
+// Joins the parts of the items that several workgroups shared.  One workgroup
+// per (head, request): dim / 4 lanes take a part, four elements each, so that
+// all parts load at once, and each lane set keeps a running maximum and sum.
+template <int DT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void paged_attention_join_kernel(const AttnArgs args,
+                                                                          const float* v_scale) {
+  // a part set's sums; every fourth lane's worth of them at most 64 * WAVES / 4
+  __shared__ floatx4 sums[64 * WAVES];
+  __shared__ float top_of[16 * WAVES], weight_of[16 * WAVES];
   const PagedAttention& a = args.a;
   const int b = (int)(blockIdx.x / a.heads), head = (int)blockIdx.x - b * a.heads, D = a.dim;
   const int items = a.kv_heads * args.chunks;
   const int per = a.heads / a.kv_heads, kvh = head / per, in_kv = head - kvh * per;
   const int i = kvh * args.chunks + in_kv / args.group, h = in_kv % args.group;
-  uint16_t* out = static_cast<uint16_t*>(a.out) + ((int64_t)b * a.heads + head) * D;
-  const int64_t from = args.tiles_before[b], tiles = args.tiles_before[b + 1] - from;
-  if (tiles == 0) {
-    for (int d = (int)threadIdx.x; d < D; d += 256) out[d] = 0;
-    return;
-  }
-  const int64_t total = (int64_t)items * args.tiles_before[a.batch];
-  const int64_t used = total < args.groups ? total : args.groups;
-  const int64_t s = from * items + i * tiles, e = s + tiles;
-  const int w0 = (int)(((s + 1) * used - 1) / total), w1 = (int)((e * used - 1) / total);
-  if (w0 == w1) return;   // one workgroup had all of it
-  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
-  auto slot = [&](int w) {
-    return args.partial + (2 * (int64_t)w + (w == w0)) * args.slot_floats;
-  };
-  float top = -INFINITY;
-  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, slot(w)[h]);
+  const uint32_t info = args.parts[(int64_t)b * items + i];
+  const int count = (int)(info & 0xffff) + 1, w0 = (int)(info >> 16);
+  if (count == 1) return;   // one workgroup had all of it, or there was nothing
+  const int lanes = D / 4, sets = 64 * WAVES / lanes;
+  const int set = (int)threadIdx.x / lanes, e = (int)threadIdx.x - set * lanes;
+  float top = -INFINITY, sum = 0.f;
+  floatx4 o = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kAtOnce = 4;
+  for (int p = set; p < count && set < sets; p += kAtOnce * sets) {
+    float pm[kAtOnce], pl[kAtOnce];
+    floatx4 po[kAtOnce];
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  const float base = top == -INFINITY ? 0.f : top;
-  // each wave takes every fourth part, a lane four of its elements
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-#pragma unroll 4
-  for (int w = w0 + wave; w <= w1; w += 4) {
-    const float* x = slot(w);
-    const float f = __builtin_amdgcn_exp2f(x[h] - base);
-    sum += f * x[kMaxGroup + h];
-    if (4 * lane < D) {
-      const floatx4 v = *reinterpret_cast<const floatx4*>(x + kSlotHead + h * D + 4 * lane);
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int q = p + j * sets < count ? p + j * sets : p;
+      const float* x = args.partial + (2 * (int64_t)(w0 + q) + (q == 0)) * args.slot_floats;
+      pm[j] = x[h];
+      pl[j] = x[kMaxGroup + h];
+      po[j] = *reinterpret_cast<const floatx4*>(x + kSlotHead + h * D + 4 * e);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] += f * v[j];
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (p + j * sets >= count) break;
+      const float y = fmaxf(top, pm[j]), base = y == -INFINITY ? 0.f : y;
+      const float f = __builtin_amdgcn_exp2f(top - base), g = __builtin_amdgcn_exp2f(pm[j] - base);
+      sum = sum * f + pl[j] * g;
+      o = o * f + po[j] * g;
+      top = y;
     }
   }
-  if (lane == 0) weights[wave] = sum;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) sums[wave][4 * lane + j] = o[j];
+  if (set < sets) {
+    sums[threadIdx.x] = o;
+    if (e == 0) {
+      top_of[set] = top;
+      weight_of[set] = sum;
+    }
+  }
   __syncthreads();
-  const int d = (int)threadIdx.x;
-  if (d >= D) return;
-  sum = weights[0] + weights[1] + weights[2] + weights[3];
-  const float y = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
-  out[d] = to_bits<DT>(sum == 0.f ? 0.f : y / sum * (v_scale ? v_scale[kvh] : 1.0f));
+  if (set > 0) return;
+  const int filled = count < sets ? count : sets;
+  for (int x = 1; x < filled; ++x) {
+    const float m = top_of[x], y = fmaxf(top, m), base = y == -INFINITY ? 0.f : y;
+    const float f = __builtin_amdgcn_exp2f(top - base), g = __builtin_amdgcn_exp2f(m - base);
+    sum = sum * f + weight_of[x] * g;
+    o = o * f + sums[x * lanes + e] * g;
+    top = y;
+  }
+  const float vs = v_scale ? v_scale[kvh] : 1.0f;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + ((int64_t)b * a.heads + head) * D + 4 * e;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = to_bits<DT>(sum == 0.f ? 0.f : o[j] / sum * vs);
 }
 
 // ---- host side ---------------------------------------------------------------
 
 constexpr int kCus = 256;
 constexpr int kMaxGroups = 4 * kCus;
-constexpr int64_t kOneItemTokens = 512;
+// One item per workgroup, and no second launch, up to that many elements of a
+// kv head's keys.  One CU reads 40 to 60 GB/s however many waves ask (four and
+// eight take the same time), which makes 768 tokens of 128 elements 10.7 us
+// (16-bit) or 9.9 us (e4m3); shared out they take 11.7 and 12.0 us, the join's
+// launch included.  At 2048 tokens it is 24.6 against 12.9 us.
+constexpr int64_t kOneItemElements = 768 * 128;
 
 struct Shares {
   int group, chunks, groups;
   int64_t slot_floats;
 };
 
-Shares shares(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dim, int64_t max_len,
-              int64_t window) {
+Shares shares(int64_t heads, int64_t kv_heads, int64_t dim, int64_t max_len, int64_t window) {
   Shares s{};
   const int64_t per = heads / kv_heads;
   s.chunks = (int)cdiv(per, kMaxGroup);
   s.group = s.chunks > 0 ? (int)cdiv(per, s.chunks) : 1;
   s.slot_floats = kSlotHead + s.group * dim;
   const int64_t span = window > 0 && window < max_len ? window : max_len;
-  if (span > kOneItemTokens) s.groups = kMaxGroups;
-  (void)batch;
+  if (span * dim > kOneItemElements) s.groups = kMaxGroups;
   return s;
+}
+
+int64_t parts_bytes(int64_t batch, int64_t kv_heads, const Shares& s) {
+  return cdiv(4 * batch * kv_heads * s.chunks, 16) * 16;
+}
+
+template <int DT>
+void launch_join(const AttnArgs& args, const float* v_scale, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)args.a.batch * args.a.heads));
+  // few workgroups may have hundreds of parts each to join, many have few
+  if (grid.x <= 2 * kCus)
+    hipLaunchKernelGGL((paged_attention_join_kernel<DT, 16>), grid, dim3(1024), 0, stream, args,
+                       v_scale);
+  else
+    hipLaunchKernelGGL((paged_attention_join_kernel<DT, 4>), grid, dim3(256), 0, stream, args,
+                       v_scale);
 }
 
 template <int DT, bool E4M3, int KS, bool FULL>
@@ -663,23 +732,23 @@ hipError_t launch_ks(AttnArgs* args, hipStream_t stream) {
 int64_t paged_attention_workspace(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dim,
                                   int64_t max_len, int64_t window) {
   if (batch == 0 || heads == 0) return 0;
-  const Shares s = shares(batch, heads, kv_heads, dim, max_len, window);
+  const Shares s = shares(heads, kv_heads, dim, max_len, window);
   if (s.groups == 0) return 0;
-  return cdiv(4 * (batch + 1), 16) * 16 + 2 * s.groups * s.slot_floats * 4;
+  return parts_bytes(batch, kv_heads, s) + 2 * s.groups * s.slot_floats * 4;
 }
 
 hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttention& a,
                                   hipStream_t stream) {
   AttnArgs args{};
   args.a = a;
-  const Shares s = shares(a.batch, a.heads, a.kv_heads, a.dim, a.max_len, a.window);
+  const Shares s = shares(a.heads, a.kv_heads, a.dim, a.max_len, a.window);
   args.group = s.group;
   args.chunks = s.chunks;
   args.groups = s.groups;
   args.slot_floats = (int)s.slot_floats;
-  args.tiles_before = static_cast<int32_t*>(a.workspace);
+  args.parts = static_cast<uint32_t*>(a.workspace);
   args.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                          cdiv(4 * ((int64_t)a.batch + 1), 16) * 16);
+                                          parts_bytes(a.batch, a.kv_heads, s));
   // 2^(s-1) < P <= 2^s: ceil(2^(31+s) / P) fits 32 bits, and n * it >> (31 + s) is n / P for
   // every n < 2^31 (the excess over n / P stays below 1 / P)
   uint32_t shift = 0;
@@ -693,9 +762,7 @@ hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttenti
                                   : (e4m3 ? launch_ks<2, true>(&args, stream)
                                           : launch_ks<2, false>(&args, stream));
   if (e != hipSuccess || s.groups == 0) return e;
-  const dim3 heads((unsigned)((int64_t)a.batch * a.heads));
-  auto join = dtype == 1 ? paged_attention_join_kernel<1> : paged_attention_join_kernel<2>;
-  hipLaunchKernelGGL(join, heads, dim3(256), 0, stream, args, e4m3 ? a.v_scale : nullptr);
+  (dtype == 1 ? launch_join<1> : launch_join<2>)(args, e4m3 ? a.v_scale : nullptr, stream);
   return hipGetLastError();
 }
 

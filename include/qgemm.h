@@ -335,7 +335,7 @@ int qgemm_w8a16_grouped(const void* x, const void* w_packed, void* y, int64_t M,
  * elements, multiples of 8), for instance the three parts of a fused QKV
  * product.  dim is a multiple of 16 up to 256.  The pools may be of any size
  * in bytes, with fewer than 2^31 slots and rows of dim elements; an append
- * takes fewer than 2^31 rows.
+ * takes tokens * kv_heads * dim / 8 below 2^31.
  */
 enum qgemm_dtype {
   QGEMM_F16 = 1,
@@ -401,7 +401,8 @@ int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
  * [kv_heads], else NULL).  Products, softmax and sums are fp32 (the
  * probabilities enter the matrix cores as the sum of two 16-bit parts), the
  * output is rounded once.  max_len is a host-side bound of lens below
- * 2^30, which sizes the launch (batch * max_len / 32 below 2^31).
+ * 2^30, which sizes the launch (batch * max_len / 32 below 2^31, batch * heads
+ * below 2^23).
  *
  * workspace: qgemm_paged_attention_workspace_bytes(...) bytes, 16-byte
  * aligned, of any contents; calls that share one must not overlap.  May be

@@ -338,10 +338,13 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = sc[i >> 2][i & 3] * kscale;
     if (counts != ~0ull) {
-      asm volatile("");   // a branch, not selects: V is waited for here only
+      // of the lanes that looked them up; formed here (and V waited for here
+      // only: a branch, not selects), eight masks kept for it took 16 registers
+      uint32_t mine = (uint32_t)(counts >> (16 * g));
+      asm volatile("" : "+v"(mine));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool ok = (counts >> (16 * g + i)) & 1;   // of the lane that looked it up
+        const bool ok = (mine >> i) & 1;
         p[i] = ok ? p[i] : -INFINITY;
 #pragma unroll
         for (int j = 0; j < VD; ++j) vr[i][j] = ok ? vr[i][j] : 0u;

@@ -6,6 +6,10 @@ tensors, allocates outputs with torch, and calls the C entry point of the same
 name on torch's current stream.  Every step of the computation runs in the
 library's HIP kernels; there is no fallback.  If libqgemm.so is missing the
 calls raise instead of computing anything.
+
+The key-value cache calls, made for every layer of a decode step, marshal their
+usual arguments in native code (_binding.so); what that does not take goes
+through the checks here.
 """
 
 import ctypes
@@ -66,6 +70,7 @@ _SIGNATURES = [
 FP8_ACT_NOALLOC_MAX_ELEMS = 16 * 1024 * 1024
 
 _lib = None
+_native = None    # the native binding, once the library is loaded
 
 
 class QgemmError(RuntimeError):
@@ -75,8 +80,9 @@ class QgemmError(RuntimeError):
 
 
 def lib():
-    """The loaded libqgemm.so (ctypes), loading it on first use."""
-    global _lib
+    """The loaded libqgemm.so (ctypes), loading it (and the native binding) on
+    first use."""
+    global _lib, _native
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
@@ -86,7 +92,12 @@ def lib():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
-        _lib = handle
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is not built for this interpreter; run "
+                               "`python -m bit_quantized_gemm_qgemm_amd.build`") from e
+        _lib, _native = handle, _binding
     return _lib
 
 
@@ -433,9 +444,9 @@ def qgemm_fp8_act_noalloc(a, b_packed, scale_b, N, out):
 
 # ---- paged key-value cache ---------------------------------------------------
 #
-# These calls are made for every layer of every decode step and the kernels
-# behind them take a few microseconds, so their checks are kept to a few
-# attribute reads per tensor; _refuse says what is wrong once something is.
+# Each call first offers its arguments to the native binding (which is there
+# once the library is loaded); a None means that they are not of the usual kind,
+# and the checks below say why or make the call.
 
 # qgemm_dtype codes; uint8 holds e4m3fn codes, as qgemm_quantize_fp8 returns them
 _HALF_TYPES = {torch.float16: 1, torch.bfloat16: 2}
@@ -520,6 +531,10 @@ def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None)
     those four tensors to write into.  tokens: how many tokens the host counts
     on (the sum of added).  cu_pages[-1] is the number of pages taken; past
     the end of free_pages entries and slots become -1."""
+    status = _native and _native.kv_plan(table, cached, added, free_pages, page_size, tokens, out)
+    if status is not None:
+        _check(status, "qgemm_kv_plan")
+        return out
     (batch, width), (table_stride,) = _view(table, _INT32, 2, "table")
     device = table.get_device()
     _dense(cached, _INT32, 1, "cached", device)
@@ -561,6 +576,9 @@ def qgemm_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     0: skipped) of the pools [pages, kv_heads, page_size, dim], in place.
     Pools of the same type take a copy; float8_e4m3fn (or uint8 code) pools
     take e4m3fn(x / scale[head]), k_scale and v_scale float32 [kv_heads]."""
+    status = _native and _native.kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    if status is not None:
+        return _check(status, "qgemm_kv_append")
     shape, k_strides = _view(k, _HALF_TYPES, 3, "k")
     device, dtype = k.get_device(), k.dtype
     v_shape, v_strides = _view(v, (dtype,), 3, "v", device)
@@ -597,6 +615,11 @@ def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scal
     workspace: uint8, at least qgemm_paged_attention_workspace_bytes(batch,
     heads, kv_heads, dim, max_len, window); allocated if None.  Returns out,
     [batch, heads, dim] of q's type."""
+    status = _native and _native.paged_attention(q, k_cache, v_cache, table, lens, k_scale, v_scale,
+                                                 window, max_len, scale, out, workspace)
+    if status is not None:
+        _check(status, "qgemm_paged_attention")
+        return out
     shape, q_strides = _view(q, _HALF_TYPES, 3, "q")
     device, dtype = q.get_device(), q.dtype
     batch, heads, dim = shape

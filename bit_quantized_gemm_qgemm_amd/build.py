@@ -1,4 +1,5 @@
-"""Build libqgemm.so in-tree with hipcc for gfx950.
+"""Build libqgemm.so in-tree with hipcc for gfx950, and _binding.so, the native
+half of the Python binding, with the host compiler.
 
     python -m bit_quantized_gemm_qgemm_amd.build [-v]
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(PKG_DIR)
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libqgemm.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["decode_gemm.hip", "tile_gemm.hip", "tile_wo256.hip", "tile_mx256.hip", "quantize.hip",
@@ -46,32 +49,60 @@ def _hipcc():
     return exe
 
 
+def _run(cmd, what, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what}:\n{res.stdout}\n{res.stderr}")
+
+
 def _compile(src, verbose):
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
     cmd = [_hipcc(), *HIPCC_FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {src}:\n{res.stdout}\n{res.stderr}")
+    _run(cmd, f"hipcc failed on {src}", verbose)
     return obj
 
 
+def _compile_binding(verbose):
+    import torch
+
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+          "-isystem", os.path.join(os.path.dirname(torch.__file__), "include"),
+          "-isystem", sysconfig.get_paths()["include"],
+          "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ failed on binding.cpp", verbose)
+    return obj
+
+
+def _link_binding(obj, verbose):
+    """By library names only: importing torch has loaded its libraries, and
+    libqgemm.so lies next to the binding."""
+    import torch
+
+    tmp = BINDING_PATH + ".tmp"
+    _run(["g++", "-shared", "-fPIC", obj, "-L", PKG_DIR, "-l:" + LIB_NAME,
+          "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-Wl,-rpath,$ORIGIN", "-o", tmp], "link of the binding failed", verbose)
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(verbose=False):
-    """Compile every HIP source for gfx950 and link libqgemm.so in the package."""
+    """Compile every HIP source for gfx950 and link libqgemm.so in the package,
+    then the binding next to it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = min(len(SOURCES), max(1, (os.cpu_count() or 2)))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding_obj = binding.result()
     tmp = LIB_PATH + ".tmp"
-    cmd = [_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp], "link failed",
+         verbose)
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj, verbose)
     return LIB_PATH
 
 

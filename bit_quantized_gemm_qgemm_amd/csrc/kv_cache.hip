@@ -9,7 +9,7 @@ namespace {
 // Plan: two running sums over the requests (tokens gained, pages gained), then
 // one slot per token.
 // ---------------------------------------------------------------------------
-// The workgroup walks the requests 256 at a time, one per thread, carrying
+// A workgroup walks the requests a tile at a time, one per thread, carrying
 // the sums of the tiles before; a tile's sums stay in LDS, where each token of
 // the tile finds its request by binary search.  A page that a request gains
 // starts at one of its new tokens (the first position that the held pages do
@@ -22,36 +22,46 @@ namespace {
 // itself (8 bytes a request, from L2) up to the end of its slice, so none
 // waits for another; the first also writes them out, and the last one's slice
 // is open so that a device sum past the host's count still gets its pages.
-constexpr int kPlanThreads = 256;
-constexpr int kPlanSlice = 1024;       // tokens per workgroup, four a thread
+//
+// All of it is latency: a tile costs two loads one after the other, two
+// barriers and the search.  So one tile and one token per thread where that is
+// possible: 1000 requests of a token each take one tile of 1024 instead of four
+// of 256 (10.2 -> 6.0 us), 131K tokens one token a thread instead of four
+// (6.8 -> 5.8 us).  Up to 256 of both keep the smaller workgroup (8 requests:
+// 3.3 us, 4.6 with 1024 threads).
+constexpr int kPlanThreadsSmall = 256, kPlanThreads = 1024;
 constexpr int kPlanGroups = 256;       // workgroups at most, one a CU
 
+template <int THREADS>
 struct PlanTile {
-  int64_t tok[kPlanThreads + 1];    // tokens of the requests before, within all
-  int64_t page[kPlanThreads];       // pages gained by the requests before
-  int cached[kPlanThreads];
-  int have[kPlanThreads];
-  int64_t wave[2][kPlanThreads / kWave];
+  int64_t tok[THREADS + 1];    // tokens of the requests before, within all
+  int64_t page[THREADS];       // pages gained by the requests before
+  int cached[THREADS];
+  int have[THREADS];
+  int64_t wave[2][THREADS / kWave];
+  int64_t pages;               // of the whole tile
 };
 
-__global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p, int64_t slice) {
-  __shared__ PlanTile s;
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_t slice) {
+  __shared__ PlanTile<THREADS> s;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t capacity = p.width * p.page_size;
   const uint32_t P = (uint32_t)p.page_size;
   const bool first = blockIdx.x == 0, last = blockIdx.x == gridDim.x - 1;
   const int64_t from = blockIdx.x * slice, to = last ? INT64_MAX : from + slice;
   int64_t tok0 = 0, page0 = 0;
-  for (int64_t b0 = 0; b0 < p.batch && (first || tok0 < to); b0 += kPlanThreads) {
+  for (int64_t b0 = 0; b0 < p.batch && (first || tok0 < to); b0 += THREADS) {
     const int64_t b = b0 + tid;
     int64_t cached = 0, added = 0, have = 0, take = 0;
     if (b < p.batch) {
       cached = p.cached[b] > 0 ? p.cached[b] : 0;
       added = p.added[b] > 0 ? p.added[b] : 0;
       const int64_t len = cached + added < capacity ? cached + added : capacity;
-      have = cdiv(cached, p.page_size);
+      // both counts are below 2^32, so the pages are too
+      have = ((uint32_t)cached + (P - 1)) / P;
       have = have < p.width ? have : p.width;
-      take = cdiv(len, p.page_size) - have;
+      take = (int64_t)(((uint64_t)len + (P - 1)) / P) - have;
       take = take > 0 ? take : 0;
       if (first) p.lens[b] = (int32_t)len;
     }
@@ -69,25 +79,30 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p, i
       s.wave[1][wave] = page;
     }
     __syncthreads();
-    for (int w = 0; w < wave; ++w) {
-      tok += s.wave[0][w];
-      page += s.wave[1][w];
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave - 1; ++w) {
+      const int64_t t = s.wave[0][w], q = s.wave[1][w];
+      if (w < wave) {
+        tok += t;
+        page += q;
+      }
     }
     s.tok[tid + 1] = tok0 + tok;
     s.page[tid] = page0 + page - take;
     s.cached[tid] = (int)cached;
     s.have[tid] = (int)have;
     if (tid == 0) s.tok[0] = tok0;
+    if (tid == THREADS - 1) s.pages = page;
     if (first && b < p.batch) {
       p.cu_tokens[b] = (int32_t)(tok0 + tok - added);
       p.cu_pages[b] = (int32_t)(page0 + page - take);
     }
-    if (tid == kPlanThreads - 1) s.wave[1][0] = page;   // the tile's pages, read after the barrier
     __syncthreads();
-    const int64_t tile_pages = s.wave[1][0], tok_end = s.tok[kPlanThreads];
+    const int64_t tile_pages = s.pages, tok_end = s.tok[THREADS];
     const int64_t t1 = tok_end < to ? tok_end : to;
-    for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < t1; t += kPlanThreads) {
-      int lo = 0, hi = kPlanThreads;   // the last request whose first token is not past t
+    const int filled = p.batch - b0 < THREADS ? (int)(p.batch - b0) : THREADS;
+    for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < t1; t += THREADS) {
+      int lo = 0, hi = filled;   // the last request whose first token is not past t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s.tok[mid] <= t) lo = mid; else hi = mid;
@@ -119,7 +134,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(const KvPlan p, i
   }
   // slots past the last token (the sums are complete where this runs at all)
   const int64_t end = to < p.tokens ? to : p.tokens;
-  for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < end; t += kPlanThreads) p.slots[t] = -1;
+  for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < end; t += THREADS) p.slots[t] = -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -216,10 +231,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvAppend a, int ro
 }  // namespace
 
 hipError_t launch_kv_plan(const KvPlan& p, hipStream_t stream) {
-  int64_t groups = cdiv(p.tokens, kPlanSlice);
+  const bool small = p.batch <= kPlanThreadsSmall && p.tokens <= kPlanThreadsSmall;
+  int64_t groups = small ? 1 : cdiv(p.tokens, kPlanThreads);
   groups = groups < 1 ? 1 : groups < kPlanGroups ? groups : kPlanGroups;
-  hipLaunchKernelGGL(kv_plan_kernel, dim3((unsigned)groups), dim3(kPlanThreads), 0, stream, p,
-                     cdiv(p.tokens, groups));
+  const dim3 grid((unsigned)groups);
+  if (small)
+    hipLaunchKernelGGL((kv_plan_kernel<kPlanThreadsSmall>), grid, dim3(kPlanThreadsSmall), 0, stream,
+                       p, p.tokens);
+  else
+    hipLaunchKernelGGL((kv_plan_kernel<kPlanThreads>), grid, dim3(kPlanThreads), 0, stream, p,
+                       cdiv(p.tokens, groups));
   return hipGetLastError();
 }
 

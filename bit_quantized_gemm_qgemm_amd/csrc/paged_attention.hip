@@ -17,8 +17,6 @@
 // The work is 4 D (K and V bytes) against 4 D group flops per token: bound by
 // the cache's bytes for every group.  What matters is bytes in flight: each
 // wave keeps one 32-token tile of K and V loading while it works on the last.
-#include <algorithm>
-
 #include "qgemm_common.h"
 
 namespace qgemm {
@@ -59,10 +57,14 @@ struct Attn {
   // probabilities and V enter the matrix cores as fp16 for e4m3 (its values
   // are exact there and fp16 keeps more bits of P), else in the cache's type
   static constexpr bool kHalfPV = E4M3 || DT == 1;
-  // fp16 probabilities are scaled by 2^15 so that the smallest ones stay
-  // normal; l carries the same factor
+  // workgroups of a CU, by the registers that a tile's K, V and sums take
+  // (127 to 158 up to 128 elements, 184 to 256 past them).  e4m3 of 128
+  // elements has room for a fourth and gains nothing by it (67.9 and 68.3 us).
   static constexpr int kResident = KS > 4 ? 2 : KS > 2 ? 3 : 4;
-  static constexpr float kBias = kHalfPV ? 15.0f : 0.0f;
+  // A factor 2^kBias on the probabilities, and so on l: fp16's smallest stay
+  // normal; bf16's sums stay finite for values up to the type's largest,
+  // however many tokens carry them (lengths are below 2^30).
+  static constexpr float kBias = kHalfPV ? 15.0f : -30.0f;
 };
 
 // x of this lane and of the lane 16 (or 32) lanes away, as the two results of

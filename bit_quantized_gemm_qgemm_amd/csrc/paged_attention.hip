@@ -11,9 +11,10 @@
 //   - the 4 tokens that a lane holds of each S^T tile are the ones that it
 //     feeds as P^T: the token order of O^T's product is chosen as the order
 //     that S^T's accumulators come in;
-//   - V is read by rows (a lane takes W consecutive elements of 8 tokens) and
+//   - V is read by rows (a lane takes W elements of 8 tokens, in pieces of up
+//     to 16 bytes that lie side by side in the 16 lanes of a token) and
 //     transposed inside the lane by byte permutes, so that instruction j of
-//     the W makes the outputs d = W m + j.
+//     the W makes the outputs d = PW m + j of its piece.
 // The work is 4 D (K and V bytes) against 4 D group flops per token: bound by
 // the cache's bytes for every group.  What matters is bytes in flight: each
 // wave keeps one 32-token tile of K and V loading while it works on the last.
@@ -52,8 +53,16 @@ struct Attn {
   // elements of one step of 32, or of two steps for e4m3
   static constexpr int KE = E4M3 ? 16 : 8;
   static constexpr int KL = KS * 8 / KE;                     // loads per row
-  static constexpr int VD = W * (E4M3 ? 1 : 2) / 4;          // dwords of W elements of V
   static constexpr int ES = E4M3 ? 1 : 2;
+  static constexpr int VD = W * ES / 4;                      // dwords of W elements of V
+  static constexpr int PW = W * ES > 16 ? 16 / ES : W;       // elements of a piece of V
+  static constexpr int PD = PW * ES / 4, NP = W / PW;        // its dwords; pieces
+  // Where the rows end with a 64-byte sector and one item reads them, they are
+  // loaded non-temporally: kept out of the caches they leave them to what is
+  // read again (128K tokens, bf16: 97 -> 80 us).  Otherwise a sector belongs to
+  // two instructions, or two items, and the caches hold it in between (270 MB in
+  // rows of 160 bytes: 61 -> 56 us, of 32 heads a kv head: 104 -> 91 us).
+  static constexpr bool kOnce = FULL;
   // probabilities and V enter the matrix cores as fp16 for e4m3 (its values
   // are exact there and fp16 keeps more bits of P), else in the cache's type
   static constexpr bool kHalfPV = E4M3 || DT == 1;
@@ -120,25 +129,27 @@ __device__ __forceinline__ floatx4 mma(uintx4 a, uintx4 b, floatx4 c) {
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// N dwords from p (16-byte pieces, or one 8- or 4-byte piece).  Non-temporal,
-// like the loads of K: each byte of the cache is used once, and kept out of
-// the caches it leaves them to what is read again (128K tokens, bf16: 97 ->
-// 80 us).
-template <int N>
+template <bool ONCE, class T>
+__device__ __forceinline__ T load(const uint8_t* p) {
+  const T* x = reinterpret_cast<const T*>(p);
+  if constexpr (ONCE) return __builtin_nontemporal_load(x);
+  return *x;
+}
+
+// N dwords from p: 1, 2 or 4.
+template <bool ONCE, int N>
 __device__ __forceinline__ void load_dwords(uint32_t* r, const uint8_t* p) {
-  if constexpr (N >= 4) {
+  if constexpr (N == 4) {
+    const uintx4 v = load<ONCE, uintx4>(p);
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uintx4 v = __builtin_nontemporal_load(reinterpret_cast<const uintx4*>(p + 16 * i));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r[4 * i + j] = v[j];
-    }
+    for (int j = 0; j < 4; ++j) r[j] = v[j];
   } else if constexpr (N == 2) {
-    const uintx2 v = __builtin_nontemporal_load(reinterpret_cast<const uintx2*>(p));
+    const uintx2 v = load<ONCE, uintx2>(p);
     r[0] = v[0];
     r[1] = v[1];
   } else {
-    r[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+    static_assert(N == 1, "4, 8 or 16 bytes");
+    r[0] = load<ONCE, uint32_t>(p);
   }
 }
 
@@ -200,7 +211,7 @@ template <int DT, bool E4M3, int KS, bool FULL>
 __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uintx4* sq, float* so, int b,
                                        int kvh, int h0, int hn, int t0, int t1, float* slot) {
   using A = Attn<DT, E4M3, KS, FULL>;
-  constexpr int W = A::W, KE = A::KE, KL = A::KL, VD = A::VD;
+  constexpr int W = A::W, KE = A::KE, KL = A::KL, VD = A::VD, PW = A::PW;
   constexpr bool kHalfPV = A::kHalfPV;
   const PagedAttention& a = args.a;
   const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
@@ -212,7 +223,12 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
   const int head_row = kvh * a.pool.head_rows;
   const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
   // lanes past the row's end read its last elements (never stored)
-  const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache) + (W * r < D ? W * r : D - W) * A::ES;
+  const uint8_t* vc[A::NP];
+#pragma unroll
+  for (int i = 0; i < A::NP; ++i) {
+    const int d = PW * (16 * i + r);
+    vc[i] = static_cast<const uint8_t*>(a.v_cache) + (d < D ? d : D - PW) * A::ES;
+  }
   const uint32_t row_bytes = (uint32_t)D * A::ES;
 
   floatx4 acc[W];
@@ -252,21 +268,24 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
 #pragma unroll
       for (int s = 0; s < KL; ++s) {
         const int d = KE * (4 * s + g);
-        kr[u][s] = __builtin_nontemporal_load(
-            reinterpret_cast<const uintx4*>(p + (FULL || d < D ? d : D - KE) * A::ES));
+        kr[u][s] = load<A::kOnce, uintx4>(p + (FULL || d < D ? d : D - KE) * A::ES);
       }
     }
   };
   auto load_v = [&](int rows) {
     const uint64_t at = (uint64_t)(uint32_t)(rows < 0 ? 0 : rows) * row_bytes;
-    load_dwords<VD>(vr[0], vc + in_group<0>(at));
-    load_dwords<VD>(vr[1], vc + in_group<1>(at));
-    load_dwords<VD>(vr[2], vc + in_group<2>(at));
-    load_dwords<VD>(vr[3], vc + in_group<3>(at));
-    load_dwords<VD>(vr[4], vc + in_group<4>(at));
-    load_dwords<VD>(vr[5], vc + in_group<5>(at));
-    load_dwords<VD>(vr[6], vc + in_group<6>(at));
-    load_dwords<VD>(vr[7], vc + in_group<7>(at));
+    auto token = [&](uint32_t* v, uint64_t at) {
+#pragma unroll
+      for (int i = 0; i < A::NP; ++i) load_dwords<A::kOnce, A::PD>(v + A::PD * i, vc[i] + at);
+    };
+    token(vr[0], in_group<0>(at));
+    token(vr[1], in_group<1>(at));
+    token(vr[2], in_group<2>(at));
+    token(vr[3], in_group<3>(at));
+    token(vr[4], in_group<4>(at));
+    token(vr[5], in_group<5>(at));
+    token(vr[6], in_group<6>(at));
+    token(vr[7], in_group<7>(at));
   };
   auto k_rows = [&](int rows, int (&x)[2]) {
     rows = rows < 0 ? 0 : rows;
@@ -433,9 +452,13 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
     float* o = so + (wave * args.group + r) * pitch;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (W * (4 * g + i) < D) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) o[W * (4 * g + i) + j] = acc[j][i];
+      for (int x = 0; x < A::NP; ++x) {
+        const int d = PW * (16 * x + 4 * g + i);
+        if (d < D) {
+#pragma unroll
+          for (int j = 0; j < PW; ++j) o[d + j] = acc[PW * x + j][i];
+        }
       }
   }
   __syncthreads();
@@ -717,8 +740,10 @@ hipError_t launch_main(AttnArgs* args, hipStream_t stream) {
 
 template <int DT, bool E4M3, int KS>
 hipError_t launch_full(AttnArgs* args, hipStream_t stream) {
-  return args->a.dim == 32 * KS ? launch_main<DT, E4M3, KS, true>(args, stream)
-                                : launch_main<DT, E4M3, KS, false>(args, stream);
+  // whole rows, each read by one item (see kOnce)
+  return args->a.dim == 32 * KS && args->chunks == 1
+             ? launch_main<DT, E4M3, KS, true>(args, stream)
+             : launch_main<DT, E4M3, KS, false>(args, stream);
 }
 
 template <int DT, bool E4M3>

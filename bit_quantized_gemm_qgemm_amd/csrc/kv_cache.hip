@@ -20,17 +20,56 @@ namespace {
 //
 // Several workgroups share the tokens in equal slices.  Each forms the sums
 // itself (8 bytes a request, from L2) up to the end of its slice, so none
-// waits for another; the first also writes them out, and the last one's slice
-// is open so that a device sum past the host's count still gets its pages.
+// waits for another; the first also writes them out.  The slices end at the
+// host's count of tokens: where the device's sum is past it, the last workgroup
+// writes the pages that begin there, page by page, so the time is bounded by
+// the table whatever the counts say.
 //
 // All of it is latency: a tile costs two loads one after the other, two
 // barriers and the search.  So one tile and one token per thread where that is
 // possible: 1000 requests of a token each take one tile of 1024 instead of four
-// of 256 (10.2 -> 6.0 us), 131K tokens one token a thread instead of four
-// (6.8 -> 5.8 us).  Up to 256 of both keep the smaller workgroup (8 requests:
-// 3.3 us, 4.6 with 1024 threads).
+// of 256, 131K tokens one token a thread instead of four.  Up to 256 of both
+// keep the smaller workgroup (8 requests: 3.3 us, 4.6 with 1024 threads).  Then
+// LDS: sums by moves between lanes and a token that tries its own request first
+// took 1000 requests from 6.0 to 4.7 us, 131K tokens from 5.8 to 5.0, 8 requests
+// from 3.3 to 3.0.
 constexpr int kPlanThreadsSmall = 256, kPlanThreads = 1024;
 constexpr int kPlanGroups = 256;       // workgroups at most, one a CU
+
+// x of the lane that a DPP control names, 0 where it names none or the row is
+// masked out.  VALU moves: as shuffles through LDS the 16 waves' sums stood in
+// line there for a third of a tile's time.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int64_t moved(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, ROWS, 0xf, false);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(0, (int)(uint32_t)((uint64_t)x >> 32), CTRL, ROWS, 0xf, false);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Inclusive sums over 16 lanes, by shifts of 1, 2, 4 and 8 within the row.
+__device__ __forceinline__ int64_t sums_of_row(int64_t x) {
+  x += moved<0x111>(x);
+  x += moved<0x112>(x);
+  x += moved<0x114>(x);
+  x += moved<0x118>(x);
+  return x;
+}
+
+// Over the wave: the last lane of a row goes to the next one (rows 1 and 3),
+// then lane 31 to the upper half.
+__device__ __forceinline__ int64_t sums_of_wave(int64_t x) {
+  x = sums_of_row(x);
+  x += moved<0x142, 0xa>(x);
+  x += moved<0x143, 0xc>(x);
+  return x;
+}
+
+__device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
 template <int THREADS>
 struct PlanTile {
@@ -38,20 +77,22 @@ struct PlanTile {
   int64_t page[THREADS];       // pages gained by the requests before
   int cached[THREADS];
   int have[THREADS];
-  int64_t wave[2][THREADS / kWave];
+  int64_t wave[2][THREADS / kWave];   // 16 waves at most
   int64_t pages;               // of the whole tile
 };
 
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_t slice) {
   __shared__ PlanTile<THREADS> s;
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kWaves = THREADS / kWave;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t capacity = p.width * p.page_size;
   const uint32_t P = (uint32_t)p.page_size;
   const bool first = blockIdx.x == 0, last = blockIdx.x == gridDim.x - 1;
-  const int64_t from = blockIdx.x * slice, to = last ? INT64_MAX : from + slice;
+  const int64_t from = blockIdx.x * slice, to = from + slice < p.tokens ? from + slice : p.tokens;
   int64_t tok0 = 0, page0 = 0;
-  for (int64_t b0 = 0; b0 < p.batch && (first || tok0 < to); b0 += THREADS) {
+  for (int64_t b0 = 0; b0 < p.batch && (first || last || tok0 < to); b0 += THREADS) {
     const int64_t b = b0 + tid;
     int64_t cached = 0, added = 0, have = 0, take = 0;
     if (b < p.batch) {
@@ -65,27 +106,16 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_
       take = take > 0 ? take : 0;
       if (first) p.lens[b] = (int32_t)len;
     }
-    int64_t tok = added, page = take;   // inclusive sums over the wave, then the tile
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int64_t t = __shfl_up(tok, off, kWave), q = __shfl_up(page, off, kWave);
-      if (lane >= off) {
-        tok += t;
-        page += q;
-      }
-    }
+    int64_t tok = sums_of_wave(added), page = sums_of_wave(take);
     if (lane == 63) {
       s.wave[0][wave] = tok;
       s.wave[1][wave] = page;
     }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / kWave - 1; ++w) {
-      const int64_t t = s.wave[0][w], q = s.wave[1][w];
-      if (w < wave) {
-        tok += t;
-        page += q;
-      }
+    if (wave > 0) {   // lane w brings wave w's total
+      const bool some = (lane & 15) < kWaves;
+      tok += lane_of(sums_of_row(some ? s.wave[0][lane & 15] : 0), wave - 1);
+      page += lane_of(sums_of_row(some ? s.wave[1][lane & 15] : 0), wave - 1);
     }
     s.tok[tid + 1] = tok0 + tok;
     s.page[tid] = page0 + page - take;
@@ -102,7 +132,13 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_
     const int64_t t1 = tok_end < to ? tok_end : to;
     const int filled = p.batch - b0 < THREADS ? (int)(p.batch - b0) : THREADS;
     for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < t1; t += THREADS) {
-      int lo = 0, hi = filled;   // the last request whose first token is not past t
+      // the last request whose first token is not past t; where every request
+      // gains one token it is this thread's own
+      int lo = 0, hi = filled;
+      if (tid < filled && s.tok[tid] <= t && t < s.tok[tid + 1]) {
+        lo = tid;
+        hi = tid + 1;
+      }
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s.tok[mid] <= t) lo = mid; else hi = mid;
@@ -122,7 +158,20 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_
         }
         if (page_no >= 0) slot = (int64_t)page_no * p.page_size + off;
       }
-      if (t < p.tokens) p.slots[t] = slot;
+      p.slots[t] = slot;
+    }
+    if (last && tok_end > p.tokens) {
+      for (int64_t x = tid; x < tile_pages; x += THREADS) {
+        const int64_t f = page0 + x;
+        int lo = 0, hi = filled;   // the last request whose first page is not past f
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s.page[mid] <= f) lo = mid; else hi = mid;
+        }
+        const int64_t pi = s.have[lo] + (f - s.page[lo]);
+        if (s.tok[lo] + pi * p.page_size - s.cached[lo] >= p.tokens)
+          p.table[(b0 + lo) * p.table_stride + pi] = f < p.num_free ? p.free_pages[f] : -1;
+      }
     }
     tok0 = tok_end;
     page0 += tile_pages;
@@ -133,8 +182,7 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_
     p.cu_pages[p.batch] = (int32_t)page0;
   }
   // slots past the last token (the sums are complete where this runs at all)
-  const int64_t end = to < p.tokens ? to : p.tokens;
-  for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < end; t += THREADS) p.slots[t] = -1;
+  for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < to; t += THREADS) p.slots[t] = -1;
 }
 
 // ---------------------------------------------------------------------------

@@ -444,9 +444,9 @@ def qgemm_fp8_act_noalloc(a, b_packed, scale_b, N, out):
 
 # ---- paged key-value cache ---------------------------------------------------
 #
-# Each call first offers its arguments to the native binding (which is there
-# once the library is loaded); a None means that they are not of the usual kind,
-# and the checks below say why or make the call.
+# A call that brings its outputs and workspace first offers its arguments to the
+# native binding (which is there once the library is loaded); a None means that
+# they are not of the usual kind, and the checks below say why or make the call.
 
 # qgemm_dtype codes; uint8 holds e4m3fn codes, as qgemm_quantize_fp8 returns them
 _HALF_TYPES = {torch.float16: 1, torch.bfloat16: 2}
@@ -531,7 +531,9 @@ def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None)
     those four tensors to write into.  tokens: how many tokens the host counts
     on (the sum of added).  cu_pages[-1] is the number of pages taken; past
     the end of free_pages entries and slots become -1."""
-    status = _native and _native.kv_plan(table, cached, added, free_pages, page_size, tokens, out)
+    status = None
+    if _native and out is not None:
+        status = _native.kv_plan(table, cached, added, free_pages, page_size, tokens, out)
     if status is not None:
         _check(status, "qgemm_kv_plan")
         return out
@@ -576,7 +578,9 @@ def qgemm_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     0: skipped) of the pools [pages, kv_heads, page_size, dim], in place.
     Pools of the same type take a copy; float8_e4m3fn (or uint8 code) pools
     take e4m3fn(x / scale[head]), k_scale and v_scale float32 [kv_heads]."""
-    status = _native and _native.kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    status = None
+    if _native:
+        status = _native.kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
     if status is not None:
         return _check(status, "qgemm_kv_append")
     shape, k_strides = _view(k, _HALF_TYPES, 3, "k")
@@ -615,8 +619,10 @@ def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scal
     workspace: uint8, at least qgemm_paged_attention_workspace_bytes(batch,
     heads, kv_heads, dim, max_len, window); allocated if None.  Returns out,
     [batch, heads, dim] of q's type."""
-    status = _native and _native.paged_attention(q, k_cache, v_cache, table, lens, k_scale, v_scale,
-                                                 window, max_len, scale, out, workspace)
+    status = None
+    if _native and out is not None and workspace is not None:
+        status = _native.paged_attention(q, k_cache, v_cache, table, lens, k_scale, v_scale, window,
+                                         max_len, scale, out, workspace)
     if status is not None:
         _check(status, "qgemm_paged_attention")
         return out

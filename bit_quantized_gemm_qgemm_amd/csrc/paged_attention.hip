@@ -628,8 +628,8 @@ void paged_attention_kernel(const AttnArgs args) {
 // per (head, request): dim / 4 lanes take a part, four elements each, so that
 // all parts load at once, and each lane set keeps a running maximum and sum.
 // 8 x 96 parts take 6 us (16 when every wave walked the parts in turn), and 4096
-// items of one to three 7 us.  Latency: two dependent loads and a launch; finding
-// the maximum first, two waves an item, or fewer loads at once measured no better.
+// items of one to three 5 us.  Latency: two dependent loads and a launch; finding
+// the maximum first measured no better.
 template <int DT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void paged_attention_join_kernel(const AttnArgs args,
                                                                           const float* v_scale) {
@@ -724,16 +724,26 @@ int64_t parts_bytes(int64_t batch, int64_t kv_heads, const Shares& s) {
   return cdiv(4 * batch * kv_heads * s.chunks, 16) * 16;
 }
 
+template <int DT, int WAVES>
+void launch_join(const AttnArgs& args, const float* v_scale, hipStream_t stream) {
+  hipLaunchKernelGGL((paged_attention_join_kernel<DT, WAVES>),
+                     dim3((unsigned)((int64_t)args.a.batch * args.a.heads)), dim3(64 * WAVES), 0,
+                     stream, args, v_scale);
+}
+
+// As many waves as let all workgroups run at once (32 waves a CU), 8 at most
+// (16 measured no better): few items may have a hundred parts each, many have
+// few.  4096 items: 68.5 us with four waves, 66.5 with two, attention included;
+// 1280 with up to 60 parts 27.7 with four, 28.9 with two.
 template <int DT>
 void launch_join(const AttnArgs& args, const float* v_scale, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)args.a.batch * args.a.heads));
-  // few workgroups may have hundreds of parts each to join, many have few
-  if (grid.x <= 2 * kCus)
-    hipLaunchKernelGGL((paged_attention_join_kernel<DT, 16>), grid, dim3(1024), 0, stream, args,
-                       v_scale);
+  const int64_t pairs = (int64_t)args.a.batch * args.a.heads;
+  if (pairs <= 4 * kCus)
+    launch_join<DT, 8>(args, v_scale, stream);
+  else if (pairs <= 8 * kCus)
+    launch_join<DT, 4>(args, v_scale, stream);
   else
-    hipLaunchKernelGGL((paged_attention_join_kernel<DT, 4>), grid, dim3(256), 0, stream, args,
-                       v_scale);
+    launch_join<DT, 2>(args, v_scale, stream);
 }
 
 template <int DT, bool E4M3, int KS, bool FULL>
@@ -801,7 +811,8 @@ hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttenti
                                   : (e4m3 ? launch_ks<2, true>(&args, stream)
                                           : launch_ks<2, false>(&args, stream));
   if (e != hipSuccess || s.groups == 0) return e;
-  (dtype == 1 ? launch_join<1> : launch_join<2>)(args, e4m3 ? a.v_scale : nullptr, stream);
+  const float* v_scale = e4m3 ? a.v_scale : nullptr;
+  dtype == 1 ? launch_join<1>(args, v_scale, stream) : launch_join<2>(args, v_scale, stream);
   return hipGetLastError();
 }
 

@@ -74,7 +74,7 @@ struct Attn {
   static constexpr bool kHalfPV = E4M3 || DT == 1;
   // 16-bit parts whose sum is a probability: bf16's three hold all 24 bits of
   // fp32; fp16's two 11 bits and, rounded to nearest, 11 more (what is left is
-  // 2^-22, or 2^-39 of the largest where that is more: see kBias).  Two parts of
+  // 2^-22, or 2^-39 of the largest where that is more: see bias).  Two parts of
   // bf16 left up to 2^-15, always towards 0, while l held all of it.  The third
   // costs nothing where bytes bound the call, and 0.1 us a tile where one wave
   // works alone: 13 requests of up to 935 tokens of 8 x 80 take 10.4 us, 9.6 with two.
@@ -83,10 +83,15 @@ struct Attn {
   // (127 to 158 up to 128 elements, 184 to 256 past them).  e4m3 of 128
   // elements has room for a fourth and gains nothing by it (67.9 and 68.3 us).
   static constexpr int kResident = KS > 4 ? 2 : KS > 2 ? 3 : 4;
-  // A factor 2^kBias on the probabilities, and so on l: fp16's smallest stay
-  // normal; bf16's sums stay finite for values up to the type's largest,
-  // however many tokens carry them (lengths are below 2^30).
-  static constexpr float kBias = kHalfPV ? 15.0f : -30.0f;
+  // A factor 2^bias on the probabilities, and so on l, the same for all parts
+  // of an item.  fp16's smallest stay normal.  bf16's add up to 1 at most over
+  // the item's n tokens: sums stay finite for values up to the type's largest,
+  // and products are no smaller than an evenly weighted mean's have to be (one
+  // token of the smallest normal value keeps it; a factor for the longest
+  // request, 2^-30, made 0 of it).
+  static __device__ __forceinline__ float bias(int n) {
+    return kHalfPV ? 15.0f : -(float)(32 - __clz(n - 1));
+  }
 };
 
 // x of this lane and of the lane 16 (or 32) lanes away, as the two results of
@@ -223,11 +228,11 @@ struct AttnShared {
 };
 
 // Tokens [t0, t1) of one item (request b, heads h0 .. h0 + hn - 1, which share
-// kv head kvh) through the waves of the workgroup; the joined result goes to
-// `out` (divided and scaled) or, unscaled, to `slot`.
+// kv head kvh, out of `span` tokens) through the waves of the workgroup; the
+// joined result goes to `out` (divided and scaled) or, unscaled, to `slot`.
 template <int DT, bool E4M3, int KS, bool FULL>
 __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uintx4* sq, float* so, int b,
-                                       int kvh, int h0, int hn, int t0, int t1, float* slot) {
+                                       int kvh, int h0, int hn, int t0, int t1, int span, float* slot) {
   using A = Attn<DT, E4M3, KS, FULL>;
   constexpr int W = A::W, KE = A::KE, KL = A::KL, VD = A::VD, PW = A::PW;
   constexpr bool kHalfPV = A::kHalfPV;
@@ -236,6 +241,7 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
   const int r = lane & 15, g = lane >> 4;
   const int D = a.dim;
 
+  const float bias = A::bias(__builtin_amdgcn_readfirstlane(span));
   const float kscale = (E4M3 ? a.k_scale[kvh] : 1.0f) * a.scale * kLog2e;
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
   const int head_row = kvh * a.pool.head_rows;
@@ -392,10 +398,10 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
     float top = p[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
-    // m is the maximum rounded up to a whole number: the factor 2^15, the
+    // m is the maximum rounded up to a whole number: the factor 2^bias, the
     // difference of two m and the shrinking by it are exact, and m moves less
     top = fmaxf(m, __builtin_ceilf(max_over_groups(top)));
-    const float base = (top == -INFINITY ? 0.f : top) - A::kBias;
+    const float base = (top == -INFINITY ? 0.f : top) - bias;
     if (__any(top != m)) {
       const float shrink = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
       l *= shrink;
@@ -535,7 +541,7 @@ void paged_attention_kernel(const AttnArgs args) {
     item_heads(args, (int)blockIdx.x - b * items, &kvh, &h0, &hn);
     int first, n;
     token_range(a, b, &first, &n);
-    attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first, n, nullptr);
+    attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first, n, n - first, nullptr);
     return;
   }
   // The places of all items (see Stretches), whatever the lengths are.
@@ -628,7 +634,7 @@ void paged_attention_kernel(const AttnArgs args) {
         args.parts[(int64_t)b * items + i] = blockIdx.x << 16 | (last - blockIdx.x);
       }
       attend<DT, E4M3, KS, FULL>(args, sh, sq, so, b, kvh, h0, hn, first + tile0 * kTileTokens,
-                                 t1 < n ? t1 : n, slot);
+                                 t1 < n ? t1 : n, n - first, slot);
     }
     pos += stop - tile0;
   }

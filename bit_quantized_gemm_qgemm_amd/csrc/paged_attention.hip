@@ -73,11 +73,11 @@ struct Attn {
   // are exact there and fp16 keeps more bits of P), else in the cache's type
   static constexpr bool kHalfPV = E4M3 || DT == 1;
   // 16-bit parts whose sum is a probability: bf16's three hold all 24 bits of
-  // fp32; fp16's two 11 bits and, rounded to nearest, 11 more (what is left is
-  // 2^-22, or 2^-39 of the largest where that is more: see bias).  Two parts of
+  // fp32; fp16's two, each rounded to nearest, 23 (what is left is 2^-23, or
+  // 2^-39 of the largest where that is more: see bias).  Two parts of
   // bf16 left up to 2^-15, always towards 0, while l held all of it.  The third
   // costs nothing where bytes bound the call, and 0.1 us a tile where one wave
-  // works alone: 13 requests of up to 935 tokens of 8 x 80 take 10.4 us, 9.6 with two.
+  // works alone: 13 requests of up to 935 tokens of 8 x 80 take 10.1 us, 9.6 with two.
   static constexpr int kParts = kHalfPV ? 2 : 3;
   // workgroups of a CU, by the registers that a tile's K, V and sums take
   // (127 to 158 up to 128 elements, 184 to 256 past them).  e4m3 of 128
@@ -226,6 +226,57 @@ struct AttnShared {
   uint32_t before;
   int request;
 };
+
+// Element d of one head's sum over tokens [t0, t1) where it came out infinite or
+// NaN and the sum of the weights did not.  The matrix cores multiply an infinite
+// value by parts of its weight that may be 0, and a weight itself may be below
+// fp32's range; but every weight of a finite score is above 0, so the sum is that
+// infinity, NaN for two of both signs, for a NaN among the values and for a
+// score of -infinity at an infinite value.  One lane reads the values again, one
+// after the other, and the key of an infinite one: slow, and only for such sums
+// (128K tokens of 8 x 128: 97 us, 17 ms if every value is infinite).
+template <int DT>
+__device__ __forceinline__ float sum_of_infinities(int b, int kvh, int head, int d, int t0, int t1,
+                                                   float sum) {
+  // the kernel's argument read anew: what only this uses takes no registers earlier
+  auto fresh = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(fresh));
+  const AttnArgs& args = *reinterpret_cast<const AttnArgs*>(fresh);
+  const PagedAttention& a = args.a;
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_batch_stride +
+                      (int64_t)head * a.q_head_stride;
+  const int head_row = kvh * a.pool.head_rows;
+  auto value = [](uint16_t bits) {
+    return DT == 1 ? (float)__builtin_bit_cast(_Float16, bits)
+                   : __builtin_bit_cast(float, (uint32_t)bits << 16);
+  };
+  bool up = false, down = false;
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    const int page = (int)(__umulhi(2u * (uint32_t)t, args.page_magic) >> args.page_shift);
+    const int e = table[page];
+    if (e < 0 || e >= a.pool.pages) continue;
+    const int row = e * a.pool.page_rows + head_row + (t - page * a.pool.page_size) * a.pool.token_rows;
+    const int64_t at = (int64_t)row * a.dim;
+    const float v = value(static_cast<const uint16_t*>(a.v_cache)[at + d]);
+    if (fabsf(v) < INFINITY) continue;
+    if (v != v) return v;
+    const uint16_t* k = static_cast<const uint16_t*>(a.k_cache) + at;
+    float s = 0.f;
+    for (int x = 0; x < a.dim; x += 8) {
+      const uintx4 qx = *reinterpret_cast<const uintx4*>(q + x), kx = *reinterpret_cast<const uintx4*>(k + x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        s = __builtin_fmaf(value((uint16_t)(qx[j >> 1] >> (16 * (j & 1)))),
+                           value((uint16_t)(kx[j >> 1] >> (16 * (j & 1)))), s);
+    }
+    if (s * (a.scale * kLog2e) == -INFINITY) return __builtin_nanf("");
+    if (v > 0.f) up = true; else down = true;
+  }
+  if (up && down) return __builtin_nanf("");
+  return up ? INFINITY : down ? -INFINITY : sum;
+}
 
 // Tokens [t0, t1) of one item (request b, heads h0 .. h0 + hn - 1, which share
 // kv head kvh, out of `span` tokens) through the waves of the workgroup; the
@@ -414,23 +465,21 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
       p[i] = __builtin_amdgcn_exp2f(p[i] - base);
       l += p[i];
     }
-    // P^T in 16-bit parts that add up to it, the later ones never 0: an infinite
-    // value of V times them has to stay infinite
+    // P^T in 16-bit parts that add up to it
     uintx4 part[A::kParts];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float x = p[2 * i], y = p[2 * i + 1];
       if constexpr (kHalfPV) {
-        const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
+        const half2_t h = __builtin_convertvector((floatx2{x, y}), half2_t);
+        const floatx2 rest = {x - (float)h[0], y - (float)h[1]};
         part[0][i] = __builtin_bit_cast(uint32_t, h);
-        const floatx2 rest = {fmaxf(x - (float)h[0], 0x1p-24f), fmaxf(y - (float)h[1], 0x1p-24f)};
         part[1][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, half2_t));
       } else {
 #pragma unroll
         for (int n = 0; n < A::kParts; ++n) {
-          const float fx = n > 0 ? fmaxf(x, 0x1p-100f) : x, fy = n > 0 ? fmaxf(y, 0x1p-100f) : y;
-          part[n][i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, fy),
-                                             __builtin_bit_cast(uint32_t, fx), 0x07060302u);
+          part[n][i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y),
+                                             __builtin_bit_cast(uint32_t, x), 0x07060302u);
           x -= truncated(x);
           y -= truncated(y);
         }
@@ -490,30 +539,44 @@ __device__ __forceinline__ void attend(const AttnArgs& args, AttnShared& sh, uin
       }
   }
   __syncthreads();
-  for (int x = (int)threadIdx.x; x < hn * D; x += 64 * kAttnWaves) {
-    const int h = x / D, d = x - h * D;
-    float top = -INFINITY;
+  auto join = [&](auto&& fix) {
+    for (int x = (int)threadIdx.x; x < hn * D; x += 64 * kAttnWaves) {
+      const int h = x / D, d = x - h * D;
+      float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sh.m[w][h]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o = 0.f;
+      for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sh.m[w][h]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(sh.m[w][h] - base);
-      sum += f * sh.l[w][h];
-      o += f * so[(w * args.group + h) * pitch + d];
-    }
-    if (slot) {
-      if (d == 0) {
-        slot[h] = top;
-        slot[kMaxGroup + h] = sum;
+      for (int w = 0; w < kAttnWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sh.m[w][h] - base);
+        sum += f * sh.l[w][h];
+        o += f * so[(w * args.group + h) * pitch + d];
       }
-      slot[kSlotHead + h * D + d] = o;
-    } else {
-      const float y = sum == 0.f ? 0.f : o / sum * (E4M3 ? a.v_scale[kvh] : 1.0f);
-      static_cast<uint16_t*>(a.out)[((int64_t)b * a.heads + h0 + h) * D + d] = to_bits<DT>(y);
+      fix(h, d, sum, o);
+      if (slot) {
+        if (d == 0) {
+          slot[h] = top;
+          slot[kMaxGroup + h] = sum;
+        }
+        slot[kSlotHead + h * D + d] = o;
+      } else {
+        const float y = sum == 0.f ? 0.f : o / sum * (E4M3 ? a.v_scale[kvh] : 1.0f);
+        static_cast<uint16_t*>(a.out)[((int64_t)b * a.heads + h0 + h) * D + d] = to_bits<DT>(y);
+      }
     }
-  }
+  };
+  auto odd = [](float sum, float o) { return !(fabsf(o) < INFINITY) && fabsf(sum) < INFINITY; };
+  // Joined once more, seldom, where infinite values met (they are only noted here: in
+  // this loop their code made short calls 0.2 us longer).
+  bool again = false;
+  join([&](int, int, float sum, float o) { again |= odd(sum, o); });
+  if constexpr (!E4M3)   // whose values are finite or NaN
+    if (__builtin_expect(again, 0))
+      join([&](int h, int d, float sum, float& o) {
+        if (odd(sum, o))
+          o = sum_of_infinities<DT>(b, kvh, h0 + h, d, t0, t1, o);
+      });
   __syncthreads();
 }
 
@@ -583,7 +646,7 @@ void paged_attention_kernel(const AttnArgs args) {
     if (b0 > 0) __syncthreads();
     scan(b0);
   }
-  const uint64_t total = (uint64_t)items * sum;
+  const uint64_t total = (uint64_t)items * (uint32_t)__builtin_amdgcn_readfirstlane(sum);
   uint64_t used = total / kMinShare;
   used = used < 1 ? 1 : used < (uint64_t)args.groups ? used : args.groups;
   const Stretches shares(total, used);
@@ -603,9 +666,10 @@ void paged_attention_kernel(const AttnArgs args) {
   }
   int b = 0;
   uint64_t before = 0;   // places of the requests before b
+  // what follows is the same in all lanes: in scalar registers it leaves the loop's alone
   if (start < end) {
-    b = sh.request;
-    before = (uint64_t)items * sh.before;
+    b = __builtin_amdgcn_readfirstlane(sh.request);
+    before = (uint64_t)items * (uint32_t)__builtin_amdgcn_readfirstlane(sh.before);
   }
   for (uint64_t pos = start; pos < end;) {
     const int tiles = tiles_of(a, b), places = places_of(tiles);
@@ -708,6 +772,22 @@ __global__ __launch_bounds__(64 * WAVES) void paged_attention_join_kernel(const 
     sum = sum * f + weight_of[x] * g;
     o = o * f + sums[x * lanes + e] * g;
     top = y;
+  }
+  // A part that is infinite weighs more than 0, whatever its factor came to.
+  if (__builtin_expect(!(fabsf(o[0]) < INFINITY && fabsf(o[1]) < INFINITY && fabsf(o[2]) < INFINITY &&
+                         fabsf(o[3]) < INFINITY), 0)) {
+    floatx4 odd = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int p = 0; p < count; ++p) {
+      const float* x = args.partial + (2 * (int64_t)(w0 + p) + (p == 0)) * args.slot_floats + kSlotHead +
+                       h * D + 4 * e;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!(fabsf(x[j]) < INFINITY)) odd[j] += x[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (odd[j] != 0.f) o[j] = odd[j];
   }
   const float vs = v_scale ? v_scale[kvh] : 1.0f;
   uint16_t* out = static_cast<uint16_t*>(a.out) + ((int64_t)b * a.heads + head) * D + 4 * e;

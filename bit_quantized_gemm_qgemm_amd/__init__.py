@@ -528,7 +528,8 @@ def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None)
     [batch, width]) gets the pages that it gains from free_pages (int32), in
     place.  Returns (lens [batch], cu_tokens [batch + 1], cu_pages
     [batch + 1], all int32, and slots int64 [tokens]); `out` may be a tuple of
-    those four tensors to write into.  tokens: how many tokens the host counts
+    those four tensors to write into, none of which may share memory with
+    another or with an input, except that lens may be cached.  tokens: how many tokens the host counts
     on (the sum of added).  cu_pages[-1] is the number of pages taken; past
     the end of free_pages entries and slots become -1."""
     status = None

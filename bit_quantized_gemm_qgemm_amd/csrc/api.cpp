@@ -311,6 +311,25 @@ int check_kv_pool(int64_t kv_heads, int64_t dim, int64_t pages, int64_t page_siz
   return QGEMM_OK;
 }
 
+// Entries of 4 bytes from `at` on.
+struct Span {
+  uintptr_t at;
+  int64_t n;
+  Span(const void* p, int64_t entries) : at(reinterpret_cast<uintptr_t>(p)), n(entries) {}
+  bool meets(const Span& o) const {
+    return n > 0 && o.n > 0 && at < o.at + 4 * (uintptr_t)o.n && o.at < at + 4 * (uintptr_t)n;
+  }
+};
+
+// Whether x meets a row of a table: rows of `width` entries, `stride` apart.
+bool meets_rows(const Span& x, const void* table, int64_t rows, int64_t width, int64_t stride) {
+  const Span all(table, rows > 0 && width > 0 ? (rows - 1) * stride + width : 0);
+  if (!x.meets(all)) return false;
+  if (rows == 1 || x.at < all.at) return true;
+  const int64_t from = (int64_t)((x.at - all.at) / 4), row = from / stride;   // stride >= width
+  return from - row * stride < width || from + x.n > (row + 1) * stride;
+}
+
 bool kv_view_ok(int64_t outer, int64_t inner) {   // strides of q, k, v: whole 16-byte pieces
   return below(outer, 0, kMaxStride) && below(inner, 0, kMaxStride) && outer % 8 == 0 &&
          inner % 8 == 0;
@@ -331,6 +350,7 @@ const char* qgemm_status_string(int status) {
     case QGEMM_ERR_FORMAT: return "unknown format id";
     case QGEMM_ERR_DEVICE: return "no HIP device available";
     case QGEMM_ERR_TOO_LARGE: return "input larger than the entry point's fixed scratch";
+    case QGEMM_ERR_OVERLAP: return "buffers share memory that must not";
     default: return "unknown status";
   }
 }
@@ -559,7 +579,8 @@ int qgemm_kv_plan(int32_t* table, const int32_t* cached, const int32_t* added,
   if (!below(batch, 0, kMaxIndex) || !below(width, 0, kMaxIndex) ||
       !below(num_free, 0, kMaxIndex) || !below(page_size, 1, kMaxIndex) ||
       !below(tokens, 0, kMaxIndex) || !below(table_stride, 0, kMaxStride) ||
-      (batch > 1 && table_stride < width))
+      (batch > 1 && table_stride < width) ||
+      (table_stride > 0 && batch > ((int64_t)1 << 60) / table_stride))   // no such table
     return QGEMM_ERR_SHAPE;
   if (!present(table, batch * width) || !present(cached, batch) || !present(added, batch) ||
       !present(free_pages, num_free) || !present(lens, batch) || !cu_tokens || !cu_pages ||
@@ -572,6 +593,19 @@ int qgemm_kv_plan(int32_t* table, const int32_t* cached, const int32_t* added,
   if (!aligned(slots, 8)) return QGEMM_ERR_ALIGN;
   int st = check_device();
   if (st != QGEMM_OK) return st;
+  // The workgroups read the inputs at any time of the launch, so nothing that it
+  // writes may lie there: but lens on cached is kept apart by the launch.
+  const Span in[] = {{cached, batch}, {added, batch}, {free_pages, num_free}};
+  const Span made[] = {{lens, batch}, {cu_tokens, batch + 1}, {cu_pages, batch + 1}, {slots, 2 * tokens}};
+  for (const Span& x : in)
+    if (meets_rows(x, table, batch, width, table_stride)) return QGEMM_ERR_OVERLAP;
+  for (const Span& x : made) {
+    if (meets_rows(x, table, batch, width, table_stride)) return QGEMM_ERR_OVERLAP;
+    for (const Span& y : in)
+      if (x.meets(y) && !(&x == made && &y == in && lens == cached)) return QGEMM_ERR_OVERLAP;
+    for (const Span& y : made)
+      if (&x != &y && x.meets(y)) return QGEMM_ERR_OVERLAP;
+  }
   return launched(qgemm::launch_kv_plan(
       qgemm::KvPlan{table, cached, added, free_pages, lens, cu_tokens, cu_pages, slots, batch,
                     width, table_stride, num_free, page_size, tokens},

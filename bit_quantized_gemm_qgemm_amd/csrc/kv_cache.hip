@@ -16,7 +16,9 @@ namespace {
 // not cover is not before the first new one), so the thread of the token at a
 // page's first position writes the table entry, and every thread takes the
 // number of a new page from the free list itself: nothing is read that this
-// launch writes.
+// launch writes.  (Lengths updated in place would be, by the other workgroups: a
+// lone one reads each count once, in the thread that then writes it; for more,
+// kv_lens_kernel writes them in a launch of its own, 1.6 us for 3000 requests.)
 //
 // Several workgroups share the tokens in equal slices.  Each forms the sums
 // itself (8 bytes a request, from L2) up to the end of its slice, so none
@@ -71,6 +73,15 @@ __device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// Tokens of a request after the step.
+__device__ __forceinline__ int64_t length_after(int64_t cached, int64_t added, int64_t capacity) {
+  return cached + added < capacity ? cached + added : capacity;
+}
+
+__device__ __forceinline__ int64_t count_of(const int32_t* counts, int64_t b) {
+  return counts[b] > 0 ? counts[b] : 0;
+}
+
 template <int THREADS>
 struct PlanTile {
   int64_t tok[THREADS + 1];    // tokens of the requests before, within all
@@ -96,15 +107,15 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_
     const int64_t b = b0 + tid;
     int64_t cached = 0, added = 0, have = 0, take = 0;
     if (b < p.batch) {
-      cached = p.cached[b] > 0 ? p.cached[b] : 0;
-      added = p.added[b] > 0 ? p.added[b] : 0;
-      const int64_t len = cached + added < capacity ? cached + added : capacity;
+      cached = count_of(p.cached, b);
+      added = count_of(p.added, b);
+      const int64_t len = length_after(cached, added, capacity);
       // both counts are below 2^32, so the pages are too
       have = ((uint32_t)cached + (P - 1)) / P;
       have = have < p.width ? have : p.width;
       take = (int64_t)(((uint64_t)len + (P - 1)) / P) - have;
       take = take > 0 ? take : 0;
-      if (first) p.lens[b] = (int32_t)len;
+      if (first && p.lens) p.lens[b] = (int32_t)len;
     }
     int64_t tok = sums_of_wave(added), page = sums_of_wave(take);
     if (lane == 63) {
@@ -183,6 +194,12 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(const KvPlan p, int64_
   }
   // slots past the last token (the sums are complete where this runs at all)
   for (int64_t t = (tok0 > from ? tok0 : from) + tid; t < to; t += THREADS) p.slots[t] = -1;
+}
+
+__global__ __launch_bounds__(256) void kv_lens_kernel(const KvPlan p) {
+  const int64_t b = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (b < p.batch)
+    p.lens[b] = (int32_t)length_after(count_of(p.cached, b), count_of(p.added, b), p.width * p.page_size);
 }
 
 // ---------------------------------------------------------------------------
@@ -283,12 +300,17 @@ hipError_t launch_kv_plan(const KvPlan& p, hipStream_t stream) {
   int64_t groups = small ? 1 : cdiv(p.tokens, kPlanThreads);
   groups = groups < 1 ? 1 : groups < kPlanGroups ? groups : kPlanGroups;
   const dim3 grid((unsigned)groups);
+  KvPlan q = p;
+  const bool lens_after = groups > 1 && p.lens == p.cached;
+  if (lens_after) q.lens = nullptr;
   if (small)
     hipLaunchKernelGGL((kv_plan_kernel<kPlanThreadsSmall>), grid, dim3(kPlanThreadsSmall), 0, stream,
-                       p, p.tokens);
+                       q, p.tokens);
   else
-    hipLaunchKernelGGL((kv_plan_kernel<kPlanThreads>), grid, dim3(kPlanThreads), 0, stream, p,
+    hipLaunchKernelGGL((kv_plan_kernel<kPlanThreads>), grid, dim3(kPlanThreads), 0, stream, q,
                        cdiv(p.tokens, groups));
+  if (lens_after && p.batch > 0)
+    hipLaunchKernelGGL(kv_lens_kernel, dim3((unsigned)cdiv(p.batch, 256)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -80,8 +80,10 @@ enum qgemm_status {
   QGEMM_ERR_LAUNCH = -5,  /* the HIP runtime reported a launch error        */
   QGEMM_ERR_FORMAT = -6,  /* unknown format id                               */
   QGEMM_ERR_DEVICE = -7,  /* no HIP device could be queried                  */
-  QGEMM_ERR_TOO_LARGE = -8  /* the input exceeds an entry point's fixed
+  QGEMM_ERR_TOO_LARGE = -8, /* the input exceeds an entry point's fixed
                                scratch (qgemm_fp8_act_noalloc)              */
+  QGEMM_ERR_OVERLAP = -9  /* buffers share memory that must not
+                             (qgemm_kv_plan)                                */
 };
 
 /* Human-readable text for a status code (static storage, never NULL). */
@@ -362,8 +364,11 @@ enum qgemm_dtype {
  *               width * P or the page missing (a negative table entry).
  * tokens is the length of slots, the sum of added that the host counts on; a
  * device sum below or above it is handled as stated.  The sums are formed in
- * 64 bits and stored as int32, so they should stay below 2^31.  One launch, no
- * workspace.
+ * 64 bits and stored as int32, so they should stay below 2^31.  No workspace.
+ * lens may be cached itself: the lengths are then updated in place (past 1024
+ * tokens by a second launch).  Any other output that shares memory with another
+ * output, an input or the table is refused (QGEMM_ERR_OVERLAP), as is an input
+ * within the table.
  */
 int qgemm_kv_plan(int32_t* table, const int32_t* cached, const int32_t* added,
                   const int32_t* free_pages, int32_t* lens, int32_t* cu_tokens,

@@ -8,12 +8,13 @@ library's HIP kernels; there is no fallback.  If libqgemm.so is missing the
 calls raise instead of computing anything.
 
 The key-value cache calls, made for every layer of a decode step, marshal their
-usual arguments in native code (_binding.so); what that does not take goes
-through the checks here.
+usual arguments in native code (the module _binding); what that does not take
+goes through the checks here, and everything where it is not built.
 """
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -70,7 +71,7 @@ _SIGNATURES = [
 FP8_ACT_NOALLOC_MAX_ELEMS = 16 * 1024 * 1024
 
 _lib = None
-_native = None    # the native binding, once the library is loaded
+_native = None    # the native binding, once the library is loaded, if there is one
 
 
 class QgemmError(RuntimeError):
@@ -80,8 +81,8 @@ class QgemmError(RuntimeError):
 
 
 def lib():
-    """The loaded libqgemm.so (ctypes), loading it (and the native binding) on
-    first use."""
+    """The loaded libqgemm.so (ctypes), loading it (and the native binding, if
+    there is one) on first use."""
     global _lib, _native
     if _lib is None:
         if not os.path.exists(LIB_PATH):
@@ -95,8 +96,11 @@ def lib():
         try:
             from . import _binding
         except ImportError as e:
-            raise RuntimeError("_binding.so is not built for this interpreter; run "
-                               "`python -m bit_quantized_gemm_qgemm_amd.build`") from e
+            _binding = None
+            warnings.warn(f"the native binding is not built for this interpreter ({e}); the "
+                          "key-value cache calls take 4 to 5 us longer.  Run "
+                          "`python -m bit_quantized_gemm_qgemm_amd.build`", RuntimeWarning,
+                          stacklevel=2)
         _lib, _native = handle, _binding
     return _lib
 
@@ -529,9 +533,10 @@ def qgemm_kv_plan(table, cached, added, free_pages, page_size, tokens, out=None)
     place.  Returns (lens [batch], cu_tokens [batch + 1], cu_pages
     [batch + 1], all int32, and slots int64 [tokens]); `out` may be a tuple of
     those four tensors to write into, none of which may share memory with
-    another or with an input, except that lens may be cached.  tokens: how many tokens the host counts
-    on (the sum of added).  cu_pages[-1] is the number of pages taken; past
-    the end of free_pages entries and slots become -1."""
+    another or with an input, except that lens may be cached.  tokens: how
+    many tokens the host counts on (the sum of added).  cu_pages[-1] is the
+    number of pages taken; past the end of free_pages entries and slots become
+    -1."""
     status = None
     if _native and out is not None:
         status = _native.kv_plan(table, cached, added, free_pages, page_size, tokens, out)

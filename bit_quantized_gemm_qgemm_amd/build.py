@@ -1,5 +1,6 @@
-"""Build libqgemm.so in-tree with hipcc for gfx950, and _binding.so, the native
-half of the Python binding, with the host compiler.
+"""Build libqgemm.so in-tree with hipcc for gfx950, and the module _binding, the
+native half of the Python binding, with the host compiler (left out, with a
+warning, where there is no g++ or no Python headers: the library does not need it).
 
     python -m bit_quantized_gemm_qgemm_amd.build [-v]
 
@@ -13,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -20,7 +22,7 @@ ROOT = os.path.dirname(PKG_DIR)
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libqgemm.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["decode_gemm.hip", "tile_gemm.hip", "tile_wo256.hip", "tile_mx256.hip", "quantize.hip",
@@ -65,6 +67,15 @@ def _compile(src, verbose):
     return obj
 
 
+def _binding_needs():
+    """What the binding's build lacks on this machine, or None."""
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None
+
+
 def _compile_binding(verbose):
     import torch
 
@@ -95,14 +106,19 @@ def build(verbose=False):
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = min(len(SOURCES), max(1, (os.cpu_count() or 2)))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_compile_binding, verbose)
+        missing = _binding_needs()
+        binding = None if missing else ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        binding_obj = binding.result()
     tmp = LIB_PATH + ".tmp"
     _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp], "link failed",
          verbose)
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj, verbose)
+    if not missing:
+        _link_binding(binding.result(), verbose)
+        return LIB_PATH
+    if os.path.exists(BINDING_PATH):   # of an earlier build, with other sources
+        os.remove(BINDING_PATH)
+    warnings.warn(f"{missing} not found: built without the native binding", RuntimeWarning)
     return LIB_PATH
 
 

@@ -400,17 +400,21 @@ int qgemm_kv_append(int dtype, int cache_dtype, const void* k, const void* v,
  * window) .. n - 1 (window 0: all n) whose page is not missing,
  *   s[t] = scale * (q[b, h] . K[t]),   out[b, h] = sum_t softmax(s)[t] V[t],
  * K and V of kv head h / (heads / kv_heads).  A request with no such token
- * gets zeros.  Tokens that are left out are never used, whatever their memory
- * holds.  The weight of a finite score is above 0 however small: an infinite
- * value makes its element infinite, two of opposite signs NaN.  q: dtype [batch, heads, dim] view; out: dtype [batch, heads, dim],
- * dense; cache_dtype is dtype or QGEMM_E4M3 (then k_scale, v_scale are fp32
- * [kv_heads], else NULL).  Products, softmax and sums are fp32, the output is
- * rounded once.  The probabilities enter the matrix cores as sums of 16-bit
- * parts: for bf16 pools three, which hold all of their 24 bits; otherwise two
- * of fp16, which hold 23 bits of those above 2^-16 of a request's largest and
- * leave up to 2^-39 of it of the rest.  max_len is a host-side bound of lens below
- * 2^30, which sizes the launch (batch * max_len / 32 below 2^31, batch * heads
- * below 2^23).
+ * gets zeros, and so does a head all of whose scores are -infinity.  Tokens
+ * that are left out are never used, whatever their memory holds.  The weight of
+ * a finite score is above 0 however small: an infinite value makes its element
+ * infinite, two of opposite signs NaN.  q: dtype [batch, heads, dim] view; out:
+ * dtype [batch, heads, dim], dense; cache_dtype is dtype or QGEMM_E4M3 (then
+ * k_scale, v_scale are fp32 [kv_heads], else NULL).
+ *
+ * Products, softmax and sums are fp32, the output is rounded once.  A dot
+ * product below fp32's range is a score of -infinity and weighs 0, one above it
+ * makes the head's output NaN.  The probabilities enter the matrix cores as sums
+ * of 16-bit parts: for bf16 pools three, which hold all of their 24 bits;
+ * otherwise two of fp16, which hold 23 bits of those above 2^-16 of a request's
+ * largest and leave up to 2^-39 of it of the rest.  max_len is a host-side bound
+ * of lens below 2^30, which sizes the launch (batch * max_len / 32 below 2^31,
+ * batch * heads below 2^23).
  *
  * workspace: qgemm_paged_attention_workspace_bytes(...) bytes, 16-byte
  * aligned, of any contents; calls that share one must not overlap.  May be

@@ -59,7 +59,8 @@ def kv_append(x, slots, cache, scale=None):
 def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, max_len=None,
                     k_scale=None, v_scale=None):
     """q [batch, heads, dim], pools [pages, kv_heads, page_size, dim] (uint8
-    codes when the scales are given).  Returns (out, weight, reach) in fp64:
+    codes when the scales are given).  A request without tokens, and a head all
+    of whose scores are -infinity, gets zeros.  Returns (out, weight, reach) in fp64:
     weight = sum_t p[t] |v[t]| (the size that errors of p and of the sum act
     on) and reach [batch, heads] = max_t scale * sum_d |q[d] k[t, d]| (the size
     that errors of a score act on)."""
@@ -88,6 +89,8 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, max_len=N
             for j in range(h * group, (h + 1) * group):
                 qj = q[b, j].astype(np.float64)
                 s = k @ qj * scale
+                if s.max() == -np.inf:      # nothing weighs anything: zeros
+                    continue
                 p = np.exp(s - s.max())
                 p /= p.sum()
                 out[b, j] = p @ v

@@ -316,8 +316,8 @@ struct Span {
   uintptr_t at;
   int64_t n;
   Span(const void* p, int64_t entries) : at(reinterpret_cast<uintptr_t>(p)), n(entries) {}
-  bool meets(const Span& o) const {
-    return n > 0 && o.n > 0 && at < o.at + 4 * (uintptr_t)o.n && o.at < at + 4 * (uintptr_t)n;
+  bool meets(const Span& o) const {   // one begins within the other
+    return n > 0 && o.n > 0 && (at - o.at < 4 * (uintptr_t)o.n || o.at - at < 4 * (uintptr_t)n);
   }
 };
 

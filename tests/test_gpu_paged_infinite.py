@@ -7,9 +7,11 @@ opposite signs NaN, and a score of -infinity, whose weight is 0, NaN.  Other
 elements of the head do not see any of it.  A finite value whose weight is out
 of fp32's range adds nothing."""
 
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import bit_quantized_gemm_qgemm_amd as qg
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +123,55 @@ def test_largest_values_at_small_weights(dtype, n, t):
         assert (torch.where(tiny, (got >= 0) & (got <= 2 * ref + tol), (got - ref).abs() <= tol)).all(), \
             (gap, got, ref)
         assert (line.others(out, 5) == 0).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,page,order", [
+    (4, 2, 16, 3, "phtd"), (6, 2, 80, 24, "pthd"), (20, 1, 96, 16, "phtd"), (3, 3, 112, 16, "phtd"),
+    (8, 2, 192, 40, "pthd"), (34, 2, 256, 16, "phtd"), (5, 5, 240, 100, "phtd"),
+])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("max_len,window", [(150, 0), (70000, 0), (70000, 97)])
+def test_infinite_values_in_all_shapes(heads, kv_heads, dim, page, order, dtype, max_len, window):
+    """Infinite and NaN values at random places, in tokens that count and in
+    those that do not (past the end, before the window, of missing pages): the
+    oracle's infinities and NaN, and everything else within the tolerance of
+    test_gpu_paged_attention.py's derivation, here with whole probabilities."""
+    print("case infinite shapes", heads, kv_heads, dim, page, order, dtype, max_len, window, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(dim + page)
+    lens = [150, 0, 1, 33, 149, 64] + ([4000] if max_len > 150 else [])
+    blocks = [-(-n // page) for n in lens]
+    pages, width = sum(blocks) + 2, max(blocks)
+    shape = {"phtd": (pages, 2, kv_heads, page, dim), "pthd": (pages, 2, page, kv_heads, dim)}[order]
+    pool = torch.randn(shape, generator=g, device="cuda").to(dtype)
+    k, v = (pool[:, j] if order == "phtd" else pool[:, j].transpose(1, 2) for j in (0, 1))
+    odd = torch.rand(v.shape, generator=g, device="cuda")
+    few = 0.5 / 150
+    v[odd < few] = INF
+    v[odd > 1 - few] = -INF
+    v[(odd > 0.5) & (odd < 0.5 + few / 8)] = float("nan")
+    q = (3 * torch.randn((len(lens), heads, dim), generator=g, device="cuda")).to(dtype)
+    order = torch.randperm(pages, generator=g, device="cuda").cpu().numpy()
+    table, at = np.full((len(lens), width), -1), 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = order[at:at + n]
+        at += n
+    table[0, 1] = -1
+    scale = 2.0 * dim ** -0.5            # scores some tens apart
+    out = qg.qgemm_paged_attention(
+        q, k, v, torch.tensor(table, dtype=torch.int32, device="cuda"),
+        torch.tensor(lens, dtype=torch.int32, device="cuda"), scale=scale, max_len=max_len,
+        window=window).double().cpu().numpy()
+    with np.errstate(all="ignore"):
+        ref, weight, reach = oracle.paged_attention(*(t.float().cpu().numpy() for t in (q, k, v)), table,
+                                                    lens, scale, window=window, max_len=max_len)
+    assert (np.isnan(out) == np.isnan(ref)).all()
+    assert ((out == INF) == (ref == INF)).all() and ((out == -INF) == (ref == -INF)).all()
+    assert np.isinf(ref).any() and np.isfinite(ref).any()
+    fine = np.isfinite(ref)
+    u = 2.0 ** -24
+    part = 0.0 if dtype == torch.bfloat16 else 2.0 ** -22
+    tol = (torch.finfo(dtype).eps / 2 * np.abs(ref) * (1 + 2.0 ** -10) + weight *
+           (2 * ((dim + 8) * u * reach[..., None] + 2.0 ** -20) + part + 4 * np.sqrt(max(lens)) * u)
+           + 2.0 ** -25)
+    err = np.abs(out[fine] - ref[fine])
+    assert (err <= tol[fine]).all(), float((err / tol[fine]).max())

@@ -6,8 +6,9 @@
 //   O^T [D x 16 heads]        += V^T [D x 32] P^T [32 x 16],  P = exp2(S - m)
 // with the running maximum m and sum l of each head kept per lane column.
 // The K index of a matrix instruction may be permuted freely as long as both
-// operands agree, and both uses of that make the kernel free of LDS and of
-// shuffles on the data path:
+// operands agree, and both uses of that keep what is loaded and what is computed
+// from it in its lane, K, V and P without LDS or shuffles (Q^T waits in LDS; row
+// numbers go round by shuffles, maxima by moves between lanes):
 //   - the 4 tokens that a lane holds of each S^T tile are the ones that it
 //     feeds as P^T: the token order of O^T's product is chosen as the order
 //     that S^T's accumulators come in;
@@ -18,7 +19,7 @@
 // The work is 4 D (K and V bytes) against 4 D group flops per token: bound by
 // the cache's bytes for every group.  What matters is bytes in flight: each
 // wave keeps one 32-token tile of K and V loading while it works on the last.
-// 128K tokens of 8 x 128, bf16, take 85.5 us (6.3 TB/s; a plain read reaches
+// 128K tokens of 8 x 128, bf16, take 85.3 us (6.3 TB/s; a plain read reaches
 // 7.1), of which 1.4 go by before the first load; neither a fourth workgroup a
 // CU, nor smaller shares, nor waves kept in step by priorities change that.
 // The join's launch adds 6 us and the gap before it.  A short call is latency:
@@ -62,12 +63,13 @@ struct Attn {
   static constexpr int VD = W * ES / 4;                      // dwords of W elements of V
   static constexpr int PW = W * ES > 16 ? 16 / ES : W;       // elements of a piece of V
   static constexpr int PD = PW * ES / 4, NP = W / PW;        // its dwords; pieces
-  // Where the rows end with a 64-byte sector and one item reads them, they are
-  // loaded non-temporally: kept out of the caches they leave them to what is
-  // read again (270 MB in rows of 256 bytes: 61 us through the caches, 56 past
-  // them).  Otherwise a sector belongs to two instructions, or two items, and the
-  // caches hold it in between (rows of 160 bytes: 56 us, and 61 past them; 32
-  // heads a kv head: 90 and 104).
+  // Rows of 32 KS elements that one item reads are loaded non-temporally: kept out
+  // of the caches they leave them to what is read again (270 MB of bf16, 128
+  // elements: 60.8 us through the caches, 54.7 past them).  Otherwise the caches
+  // serve a second read: lanes past a shorter row's end take its last elements
+  // again (80 elements: 57.8 us, and 62.3 past them; 160, though whole sectors,
+  // 62.0 and 65.6; 224 73.3 and 78.0), or further items all of it (32 heads a kv
+  // head: 90 and 103).
   static constexpr bool kOnce = FULL;
   // probabilities and V enter the matrix cores as fp16 for e4m3 (its values
   // are exact there and fp16 keeps more bits of P), else in the cache's type
@@ -80,7 +82,8 @@ struct Attn {
   // works alone: 13 requests of up to 935 tokens of 8 x 80 take 10.1 us, 9.6 with two.
   static constexpr int kParts = kHalfPV ? 2 : 3;
   // workgroups of a CU, by the registers that a tile's K, V and sums take
-  // (127 to 158 up to 128 elements, 184 to 256 past them).  e4m3 of 128
+  // (98 to 115 up to 64 elements, 126 to 167 up to 128, 179 to 256 past them,
+  // where 16-bit rows of 208 or 240 elements spill 8 to 15).  e4m3 of 128
   // elements has room for a fourth and gains nothing by it (67.9 and 68.3 us).
   static constexpr int kResident = KS > 4 ? 2 : KS > 2 ? 3 : 4;
   // A factor 2^bias on the probabilities, and so on l, the same for all parts
@@ -801,9 +804,13 @@ constexpr int kCus = 256;
 constexpr int kMaxGroups = 4 * kCus;
 // One item per workgroup, and no second launch, up to that many elements of a
 // kv head's keys.  One CU reads 40 to 60 GB/s however many waves ask (four and
-// eight take the same time), which makes 768 tokens of 128 elements 10.7 us
-// (16-bit) or 9.9 us (e4m3); shared out they take 11.7 and 12.0 us, the join's
-// launch included.  At 2048 tokens it is 24.6 against 12.9 us.
+// eight take the same time), which makes 768 tokens of 128 elements 10.8 us
+// (bf16) or 9.7 us (e4m3); shared out they take 12.0 and 11.6 us, the join's
+// launch included.  At 2048 tokens it is 24.6 against 12.9 us.  Other sizes, one
+// request of 8 kv heads each: 1024 tokens of 64 elements 9.1 and 10.8, 256 of 256
+// elements 10.4 and 14.9; 16 requests of 768 x 128 16.2 and 19.5.  The rule goes
+// by max_len, so a caller that passes the most it serves shares short requests
+// out too: 204 tokens 11.0 us with a max_len of 8192, 6.3 with their own.
 constexpr int64_t kOneItemElements = 768 * 128;
 
 struct Shares {

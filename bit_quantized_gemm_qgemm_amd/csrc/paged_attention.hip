@@ -83,7 +83,8 @@ struct Attn {
   static constexpr int kParts = kHalfPV ? 2 : 3;
   // workgroups of a CU, by the registers that a tile's K, V and sums take
   // (98 to 115 up to 64 elements, 126 to 167 up to 128, 179 to 256 past them,
-  // where 16-bit rows of 208 or 240 elements spill 8 to 15).  e4m3 of 128
+  // where 16-bit rows of 208 elements on spill 8 to 15 if they are not whole or
+  // several items read them).  e4m3 of 128
   // elements has room for a fourth and gains nothing by it (67.9 and 68.3 us).
   static constexpr int kResident = KS > 4 ? 2 : KS > 2 ? 3 : 4;
   // A factor 2^bias on the probabilities, and so on l, the same for all parts

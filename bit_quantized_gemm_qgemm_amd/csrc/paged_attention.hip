@@ -72,14 +72,14 @@ struct Attn {
   // head: 90 and 103).
   static constexpr bool kOnce = FULL;
   // probabilities and V enter the matrix cores as fp16 for e4m3 (its values
-  // are exact there and fp16 keeps more bits of P), else in the cache's type
+  // are exact there, and P takes two parts of fp16), else in the cache's type
   static constexpr bool kHalfPV = E4M3 || DT == 1;
   // 16-bit parts whose sum is a probability: bf16's three hold all 24 bits of
   // fp32; fp16's two, each rounded to nearest, 23 (what is left is 2^-23, or
   // 2^-39 of the largest where that is more: see bias).  Two parts of
   // bf16 left up to 2^-15, always towards 0, while l held all of it.  The third
-  // costs nothing where bytes bound the call, and 0.1 us a tile where one wave
-  // works alone: 13 requests of up to 935 tokens of 8 x 80 take 10.1 us, 9.6 with two.
+  // costs nothing where bytes bound the call; where waves wait for one tile after
+  // the other, 13 requests of up to 935 tokens of 8 x 80 take 10.1 us, 9.6 with two.
   static constexpr int kParts = kHalfPV ? 2 : 3;
   // workgroups of a CU, by the registers that a tile's K, V and sums take
   // (98 to 115 up to 64 elements, 126 to 167 up to 128, 179 to 256 past them,

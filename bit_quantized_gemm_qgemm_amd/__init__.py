@@ -1,5 +1,6 @@
 """Python binding of libqgemm (quantized GEMMs dequantized inside the kernel,
-and the paged key-value cache of a decode step).
+products of 8-bit integers, dense or grouped by expert, and the paged key-value
+cache of a decode step).
 
 Argument marshalling only: each function checks dtypes and shapes of torch
 tensors, allocates outputs with torch, and calls the C entry point of the same
@@ -63,6 +64,16 @@ _SIGNATURES = [
     ("qgemm_paged_attention_workspace_bytes", ctypes.c_int64, [_I64] * 6),
     ("qgemm_paged_attention", ctypes.c_int,
      [ctypes.c_int, ctypes.c_int] + [_P] * 9 + [_I64] * 15 + [ctypes.c_float, _P]),
+    ("qgemm_quantize_int8", ctypes.c_int, [ctypes.c_int, _P, _P, _P, _I64, _I64, _I64, _P]),
+    ("qgemm_prepack_w8a8_bytes", ctypes.c_int64, [_I64, _I64, _I64, ctypes.c_int]),
+    ("qgemm_prepack_w8a8", ctypes.c_int, [_P, _P, _I64, _I64, _I64, ctypes.c_int, _P]),
+    ("qgemm_w8a8", ctypes.c_int,
+     [ctypes.c_int] + [_P] * 5 + [_I64] * 3 + [ctypes.c_int, _P]),
+    ("qgemm_w8a8_experts", ctypes.c_int,
+     [ctypes.c_int] + [_P] * 7 + [_I64] * 5 + [ctypes.c_int, _P]),
+    ("qgemm_expert_plan_workspace_bytes", ctypes.c_int64, [_I64] * 3),
+    ("qgemm_expert_plan", ctypes.c_int, [ctypes.c_int] + [_P] * 5 + [_I64] * 3 + [_P]),
+    ("qgemm_expert_combine", ctypes.c_int, [ctypes.c_int] + [_P] * 4 + [_I64] * 4 + [_P]),
     ("qgemm_read_probe", ctypes.c_int, [_P, _I64, _P, _I64, _P]),
     ("qgemm_mfma_probe", ctypes.c_int, [ctypes.c_int, _P, _I64, _P, _I64, _P]),
 ]
@@ -666,6 +677,223 @@ def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scal
         batch, heads, kv_heads, dim, *q_strides, pages, page_size, *strides, width, table_stride,
         max_len, window, dim ** -0.5 if scale is None else scale, _stream(q)),
         "qgemm_paged_attention")
+    return out
+
+
+# ---- int8 x int8 products, dense and by expert ---------------------------------
+
+_ROW_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 4}
+_INT8 = (torch.int8,)
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _launch(device, name, *args):
+    """Call a library function with the tensors' device as the current one."""
+    fn = getattr(lib(), name)
+    if device < 0 or torch._C._cuda_getDevice() == device:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    _check(status, name)
+
+
+def _result(out, shape, dtype, device, like):
+    """The caller's output, checked, or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dense(out, (dtype,), len(shape), "out", device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must be {list(shape)}, got {list(out.shape)}")
+    return out
+
+
+def qgemm_quantize_int8(x, out=None):
+    """Codes int8 [rows, K] and scales float32 [rows] of x [rows, K] (float16,
+    bfloat16 or float32, rows any stride apart): scale = max |x| / 127 of the
+    row, codes = x / scale to the nearest whole number.  A row with an infinity
+    or a NaN gets the scale NaN and codes of 0.  `out` may be a tuple of those
+    two tensors to write into."""
+    (rows, K), (row_stride,) = _view(x, _ROW_TYPES, 2, "x")
+    device = x.get_device()
+    if out is None:
+        out = (torch.empty((rows, K), dtype=torch.int8, device=x.device),
+               torch.empty(rows, dtype=torch.float32, device=x.device))
+        codes, scale = out
+    else:
+        out = tuple(out)
+        if len(out) != 2:
+            raise ValueError("out must be (codes, scale)")
+        codes, scale = out
+        _dense(codes, _INT8, 2, "codes", device)
+        _dense(scale, _FLOAT32, 1, "scale", device)
+        if codes.shape != x.shape or scale.shape[0] != rows:
+            raise ValueError(f"codes must be [{rows}, {K}] and scale [{rows}]")
+    _launch(device, "qgemm_quantize_int8", _ROW_TYPES[x.dtype], x.data_ptr(), codes.data_ptr(),
+            scale.data_ptr(), rows, K, row_stride, _stream(x))
+    return out
+
+
+def qgemm_prepack_w8a8_bytes(experts, K, N, gated=False):
+    n = lib().qgemm_prepack_w8a8_bytes(int(experts), int(K), int(N), int(gated))
+    if n < 0:
+        raise QgemmError(int(n), "qgemm_prepack_w8a8_bytes")
+    return int(n)
+
+
+def qgemm_prepack_w8a8(w, gated=False):
+    """int8 weight [K, N], or [experts, K, N] -> opaque packed uint8 device tensor
+    for qgemm_w8a8 / qgemm_w8a8_experts.  gated: the N columns are two halves,
+    gate and up."""
+    _need(w, torch.int8, 2 if isinstance(w, torch.Tensor) and w.dim() == 2 else 3, "w")
+    experts, K, N = (1, *w.shape) if w.dim() == 2 else w.shape
+    nbytes = qgemm_prepack_w8a8_bytes(experts, K, N, gated)
+    out = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=w.device)
+    _launch(w.get_device(), "qgemm_prepack_w8a8", w.data_ptr(), out.data_ptr(), experts, K, N,
+            int(gated), _stream(w))
+    return out
+
+
+def _w8a8_operands(a, a_scale, w_packed, experts, N, gated):
+    """Check what both products take; returns (device, rows of a, K)."""
+    if not isinstance(a, torch.Tensor):
+        raise TypeError("a must be a torch tensor")
+    device = a.get_device()
+    _dense(a, _INT8, 2, "a", device)
+    _dense(a_scale, _FLOAT32, 1, "a_scale", device)
+    _dense(w_packed, _UINT8, 1, "w_packed", device)
+    a_rows, K = a.shape
+    if a_scale.shape[0] != a_rows:
+        raise ValueError(f"a_scale must have {a_rows} entries, one per row of a")
+    if w_packed.shape[0] < qgemm_prepack_w8a8_bytes(experts, K, N, gated):
+        raise ValueError("w_packed is smaller than the packed size for these experts, K, N")
+    return device, a_rows, K
+
+
+def qgemm_w8a8(a, a_scale, w_packed, w_scale, N, gated=False, dtype=torch.bfloat16, out=None):
+    """Y = (A @ W) * a_scale[:, None] * w_scale -> `dtype` (float16 or bfloat16; that
+    of out, if given) [M, N]; gated: silu(Y[:, :N/2]) * Y[:, N/2:], [M, N/2].
+
+    a: int8 [M, K] codes and a_scale float32 [M], as qgemm_quantize_int8 gives
+    them; w_packed from qgemm_prepack_w8a8 with the same `gated`; w_scale
+    float32 [N]."""
+    N = int(N)
+    device, M, K = _w8a8_operands(a, a_scale, w_packed, 1, N, gated)
+    _dense(w_scale, _FLOAT32, 1, "w_scale", device)
+    if w_scale.shape[0] != N:
+        raise ValueError(f"w_scale must have {N} entries")
+    dtype = dtype if out is None else getattr(out, "dtype", None)
+    if dtype not in _HALF_TYPES:
+        raise TypeError(f"the output must be float16 or bfloat16, not {dtype}")
+    out = _result(out, (M, N // 2 if gated else N), dtype, device, a)
+    _launch(device, "qgemm_w8a8", _HALF_TYPES[dtype], a.data_ptr(), a_scale.data_ptr(),
+            w_packed.data_ptr(), w_scale.data_ptr(), out.data_ptr(), M, N, K, int(gated), _stream(a))
+    return out
+
+
+def qgemm_w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows=None, gated=False,
+                       dtype=torch.bfloat16, out=None):
+    """qgemm_w8a8 with a weight for each stretch of rows: rows offsets[e] to
+    offsets[e + 1] of the output take expert e's.
+
+    w_packed is of [experts, K, N], w_scale float32 [experts, N], offsets int32
+    [experts + 1].  rows, int32 [M], names the row of a (and a_scale) that each
+    of the M output rows reads; without it row m reads row m.  Rows that no
+    expert has are left as they were."""
+    N = int(N)
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a torch tensor")
+    experts = offsets.numel() - 1
+    device, a_rows, K = _w8a8_operands(a, a_scale, w_packed, experts, N, gated)
+    _dense(offsets, _INT32, 1, "offsets", device)
+    _dense(w_scale, _FLOAT32, 2, "w_scale", device)
+    if tuple(w_scale.shape) != (experts, N):
+        raise ValueError(f"w_scale must be [{experts}, {N}]")
+    M = a_rows
+    if rows is not None:
+        _dense(rows, _INT32, 1, "rows", device)
+        M = rows.shape[0]
+    dtype = dtype if out is None else getattr(out, "dtype", None)
+    if dtype not in _HALF_TYPES:
+        raise TypeError(f"the output must be float16 or bfloat16, not {dtype}")
+    out = _result(out, (M, N // 2 if gated else N), dtype, device, a)
+    _launch(device, "qgemm_w8a8_experts", _HALF_TYPES[dtype], a.data_ptr(), a_scale.data_ptr(),
+            w_packed.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(),
+            None if rows is None else rows.data_ptr(), out.data_ptr(), a_rows, M, N, K, experts,
+            int(gated), _stream(a))
+    return out
+
+
+def qgemm_expert_plan_workspace_bytes(tokens, top, experts):
+    n = lib().qgemm_expert_plan_workspace_bytes(int(tokens), int(top), int(experts))
+    if n < 0:
+        raise QgemmError(int(n), "qgemm_expert_plan_workspace_bytes")
+    return int(n)
+
+
+def qgemm_expert_plan(ids, experts, out=None, workspace=None):
+    """The order of a batch's rows, on the device.
+
+    ids: int32 or int64 [tokens, top], the experts that each token goes to; one
+    outside 0 .. experts - 1 has no row.  Returns (offsets [experts + 1], rows
+    [tokens * top], places [tokens, top]), all int32: the rows sorted by expert,
+    in their own order within one; rows[m] is the token of row m (-1 from
+    offsets[-1] on), places[t, j] the row of a token's choice (-1: none).
+    `out` may be a tuple of those three to write into; workspace: uint8, at least
+    qgemm_expert_plan_workspace_bytes(tokens, top, experts), allocated if None."""
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch tensor")
+    device, experts = ids.get_device(), int(experts)
+    _dense(ids, _ID_BYTES, 2, "ids", device)
+    tokens, top = ids.shape
+    need = qgemm_expert_plan_workspace_bytes(tokens, top, experts)
+    if out is None:
+        i32 = {"dtype": torch.int32, "device": ids.device}
+        out = (torch.empty(experts + 1, **i32), torch.empty(tokens * top, **i32),
+               torch.empty((tokens, top), **i32))
+        offsets, rows, places = out
+    else:
+        out = tuple(out)
+        if len(out) != 3:
+            raise ValueError("out must be (offsets, rows, places)")
+        offsets, rows, places = out
+        _dense(offsets, _INT32, 1, "offsets", device)
+        _dense(rows, _INT32, 1, "rows", device)
+        _dense(places, _INT32, 2, "places", device)
+        if (offsets.shape[0] != experts + 1 or rows.shape[0] != tokens * top
+                or places.shape != ids.shape):
+            raise ValueError(f"offsets, rows and places must be [{experts + 1}], [{tokens * top}] "
+                             f"and {list(ids.shape)}")
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=ids.device)
+    else:
+        _dense(workspace, _UINT8, 1, "workspace", device)
+        if workspace.shape[0] < need:
+            raise ValueError(f"workspace needs {need} bytes")
+    _launch(device, "qgemm_expert_plan", _ID_BYTES[ids.dtype], ids.data_ptr(), offsets.data_ptr(),
+            rows.data_ptr(), places.data_ptr(), workspace.data_ptr(), tokens, top, experts,
+            _stream(ids))
+    return out
+
+
+def qgemm_expert_combine(y, places, gates, out=None):
+    """out[t] = sum over j of gates[t, j] * y[places[t, j]], in fp32 and in the
+    order of j, rounded once: y [rows, N] float16 or bfloat16, places int32
+    [tokens, top] (outside 0 .. rows - 1: left out), gates float32 [tokens, top].
+    Returns out, [tokens, N] of y's type."""
+    if not isinstance(y, torch.Tensor):
+        raise TypeError("y must be a torch tensor")
+    device = y.get_device()
+    _dense(y, _HALF_TYPES, 2, "y", device)
+    _dense(places, _INT32, 2, "places", device)
+    _dense(gates, _FLOAT32, 2, "gates", device)
+    if gates.shape != places.shape:
+        raise ValueError(f"gates must be {list(places.shape)} like places, got {list(gates.shape)}")
+    rows, N = y.shape
+    tokens, top = places.shape
+    out = _result(out, (tokens, N), y.dtype, device, y)
+    _launch(device, "qgemm_expert_combine", _HALF_TYPES[y.dtype], y.data_ptr(), places.data_ptr(),
+            gates.data_ptr(), out.data_ptr(), rows, tokens, top, N, _stream(y))
     return out
 
 

@@ -27,7 +27,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["decode_gemm.hip", "tile_gemm.hip", "tile_wo256.hip", "tile_mx256.hip", "quantize.hip",
            "prepack.hip", "probes.hip", "kv_cache.hip", "paged_attention.hip",
-           "api.cpp"]
+           "w8a8.hip", "experts.hip", "api.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -330,6 +330,88 @@ bool meets_rows(const Span& x, const void* table, int64_t rows, int64_t width, i
   return from - row * stride < width || from + x.n > (row + 1) * stride;
 }
 
+// ---- int8 x int8 products, dense and by expert ------------------------------
+
+// Bytes at `at`; whether two such stretches share any.
+struct Bytes {
+  uintptr_t at;
+  uint64_t n;
+  Bytes(const void* p, int64_t bytes) : at(reinterpret_cast<uintptr_t>(p)), n((uint64_t)bytes) {}
+  bool meets(const Bytes& o) const {
+    return n > 0 && o.n > 0 && (at - o.at < o.n || o.at - at < n);
+  }
+};
+
+// Whether an output shares memory with an input or with another output.
+int check_apart(std::initializer_list<Bytes> outputs, std::initializer_list<Bytes> inputs) {
+  for (const Bytes& x : outputs) {
+    for (const Bytes& y : inputs)
+      if (x.meets(y)) return QGEMM_ERR_OVERLAP;
+    for (const Bytes& y : outputs)
+      if (&x != &y && x.meets(y)) return QGEMM_ERR_OVERLAP;
+  }
+  return QGEMM_OK;
+}
+
+// The sum of K products of two codes stays within 32 bits: 2^14 K < 2^31.
+constexpr int64_t kMaxInt8K = 131056;
+
+// One packed weight stays below 2^31 bytes (32-bit offsets within it), all of
+// them below 2^40.
+int check_w8a8_weight(int64_t experts, int64_t K, int64_t N, int gated) {
+  if (!below(experts, 1, qgemm::kMaxExperts + 1) || !below(K, 0, kMaxInt8K + 1) || K % 16 != 0 ||
+      !below(N, 0, kMaxIndex) || (gated != 0 && gated != 1) || (gated && N % 2 != 0))
+    return QGEMM_ERR_SHAPE;
+  if ((N + 32) * qgemm::cdiv(K, 128) * 128 >= kMaxIndex) return QGEMM_ERR_SHAPE;
+  return QGEMM_OK;
+}
+
+// Checks and the launch shared by qgemm_w8a8 (experts = 0) and qgemm_w8a8_experts.
+int w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
+         const float* w_scale, const int32_t* offsets, const int32_t* rows, void* out,
+         int64_t a_rows, int64_t M, int64_t N, int64_t K, int64_t experts, int gated, void* stream) {
+  if (dtype != QGEMM_F16 && dtype != QGEMM_BF16) return QGEMM_ERR_FORMAT;
+  const bool grouped = experts != 0;
+  const int64_t weights = grouped ? experts : 1;
+  int st = check_w8a8_weight(weights, K, N, gated);
+  if (st != QGEMM_OK) return st;
+  const int64_t out_n = gated ? N / 2 : N;
+  if (!below(M, 0, kMaxIndex) || !below(a_rows, 0, kMaxIndex) || a_rows * K >= kMaxIndex ||
+      M * N >= kMaxIndex || (!rows && M > 0 && a_rows != M))
+    return QGEMM_ERR_SHAPE;
+  const bool some = M > 0 && N > 0;
+  if (!present(a, a_rows * K) || !present(a_scale, a_rows) || !present(w_packed, K * N) ||
+      !present(w_scale, N) || !present(out, M * out_n) || (grouped && !offsets))
+    return QGEMM_ERR_NULL;
+  if (!aligned(a, 16) || !aligned(w_packed, 16) || !aligned(out, 16) || !aligned(a_scale, 4) ||
+      !aligned(w_scale, 4) || !aligned(offsets, 4) || !aligned(rows, 4))
+    return QGEMM_ERR_ALIGN;
+  const qgemm::W8a8Geom geom = qgemm::w8a8_geom(K, N, gated);
+  if ((st = check_apart({{out, 2 * M * out_n}},
+                        {{a, a_rows * K}, {a_scale, 4 * a_rows}, {w_packed, weights * geom.bytes},
+                         {w_scale, 4 * weights * N}, {offsets, grouped ? 4 * (experts + 1) : 0},
+                         {rows, rows ? 4 * M : 0}})) != QGEMM_OK)
+    return st;
+  if (!some) return QGEMM_OK;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  qgemm::W8a8 p{};
+  p.a = a;
+  p.a_scale = a_scale;
+  p.w = static_cast<const uint8_t*>(w_packed);
+  p.w_scale = w_scale;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.out = static_cast<uint16_t*>(out);
+  p.a_rows = a_rows;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.experts = weights;
+  p.gated = gated != 0;
+  p.bf16 = dtype == QGEMM_BF16;
+  return launched(qgemm::launch_w8a8(p, as_stream(stream)));
+}
+
 bool kv_view_ok(int64_t outer, int64_t inner) {   // strides of q, k, v: whole 16-byte pieces
   return below(outer, 0, kMaxStride) && below(inner, 0, kMaxStride) && outer % 8 == 0 &&
          inner % 8 == 0;
@@ -721,6 +803,119 @@ int qgemm_paged_attention(int dtype, int cache_dtype, const void* q, const void*
   a.window = window;
   a.scale = scale;
   return launched(qgemm::launch_paged_attention(dtype, cache_dtype, a, as_stream(stream)));
+}
+
+// ---- int8 x int8 products, dense and by expert ------------------------------
+
+int qgemm_quantize_int8(int dtype, const void* x, int8_t* codes, float* scale, int64_t rows,
+                        int64_t K, int64_t row_stride, void* stream) {
+  if (dtype != QGEMM_F16 && dtype != QGEMM_BF16 && dtype != QGEMM_F32) return QGEMM_ERR_FORMAT;
+  const int64_t size = dtype == QGEMM_F32 ? 4 : 2;
+  if (!below(rows, 0, kMaxIndex) || !below(K, 0, kMaxInt8K + 1) || K % 16 != 0 ||
+      !below(row_stride, 0, kMaxStride) || (K > 0 && row_stride * size % 16 != 0) ||
+      (row_stride > 0 && rows > ((int64_t)1 << 60) / row_stride))   // no such array
+    return QGEMM_ERR_SHAPE;
+  if (!present(x, rows * K) || !present(codes, rows * K) || !present(scale, rows))
+    return QGEMM_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return QGEMM_ERR_ALIGN;
+  if (rows == 0) return QGEMM_OK;
+  const int64_t reach = K > 0 ? size * ((rows - 1) * row_stride + K) : 0;
+  int st = check_apart({{codes, rows * K}, {scale, 4 * rows}}, {{x, reach}});
+  if (st != QGEMM_OK) return st;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  return launched(qgemm::launch_quantize_int8(dtype, x, row_stride, codes, scale, rows, K,
+                                              as_stream(stream)));
+}
+
+int64_t qgemm_prepack_w8a8_bytes(int64_t experts, int64_t K, int64_t N, int gated) {
+  const int st = check_w8a8_weight(experts, K, N, gated);
+  if (st != QGEMM_OK) return st;
+  return experts * qgemm::w8a8_geom(K, N, gated).bytes;
+}
+
+int qgemm_prepack_w8a8(const int8_t* w, void* w_packed, int64_t experts, int64_t K, int64_t N,
+                       int gated, void* stream) {
+  int st = check_w8a8_weight(experts, K, N, gated);
+  if (st != QGEMM_OK) return st;
+  const int64_t bytes = experts * qgemm::w8a8_geom(K, N, gated).bytes;
+  if (!present(w, K * N) || !present(w_packed, bytes)) return QGEMM_ERR_NULL;
+  if (!aligned(w, 16) || !aligned(w_packed, 16)) return QGEMM_ERR_ALIGN;
+  if ((st = check_apart({{w_packed, bytes}}, {{w, experts * K * N}})) != QGEMM_OK) return st;
+  if (bytes == 0) return QGEMM_OK;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  return launched(qgemm::launch_prepack_w8a8(w, w_packed, experts, K, N, gated != 0, as_stream(stream)));
+}
+
+int qgemm_w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
+               const float* w_scale, void* out, int64_t M, int64_t N, int64_t K, int gated,
+               void* stream) {
+  return w8a8(dtype, a, a_scale, w_packed, w_scale, nullptr, nullptr, out, M, M, N, K, 0, gated, stream);
+}
+
+int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
+                       const float* w_scale, const int32_t* offsets, const int32_t* rows, void* out,
+                       int64_t a_rows, int64_t M, int64_t N, int64_t K, int64_t experts, int gated,
+                       void* stream) {
+  if (experts < 1) return QGEMM_ERR_SHAPE;
+  return w8a8(dtype, a, a_scale, w_packed, w_scale, offsets, rows, out, a_rows, M, N, K, experts, gated,
+              stream);
+}
+
+int64_t qgemm_expert_plan_workspace_bytes(int64_t tokens, int64_t top, int64_t experts) {
+  if (!below(tokens, 0, kMaxIndex) || !below(top, 0, kMaxIndex) ||
+      !below(experts, 1, qgemm::kMaxExperts + 1) || tokens * top > qgemm::kMaxPairs)
+    return QGEMM_ERR_SHAPE;
+  return qgemm::expert_plan_workspace(tokens * top, experts);
+}
+
+int qgemm_expert_plan(int id_bytes, const void* ids, int32_t* offsets, int32_t* rows,
+                      int32_t* places, void* workspace, int64_t tokens, int64_t top,
+                      int64_t experts, void* stream) {
+  if (id_bytes != 4 && id_bytes != 8) return QGEMM_ERR_FORMAT;
+  const int64_t need = qgemm_expert_plan_workspace_bytes(tokens, top, experts);
+  if (need < 0) return (int)need;
+  const int64_t pairs = tokens * top;
+  if (!present(ids, pairs) || !offsets || !present(rows, pairs) || !present(places, pairs) ||
+      !present(workspace, need))
+    return QGEMM_ERR_NULL;
+  if (!aligned(ids, (uintptr_t)id_bytes) || !aligned(offsets, 4) || !aligned(rows, 4) ||
+      !aligned(places, 4) || !aligned(workspace, 16))
+    return QGEMM_ERR_ALIGN;
+  // ids are read while the outputs are written
+  int st = check_apart({{offsets, 4 * (experts + 1)}, {rows, 4 * pairs}, {places, 4 * pairs},
+                        {workspace, need}},
+                       {{ids, id_bytes * pairs}});
+  if (st != QGEMM_OK) return st;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  return launched(qgemm::launch_expert_plan(
+      qgemm::ExpertPlan{ids, id_bytes == 8, offsets, rows, places, static_cast<int32_t*>(workspace),
+                        pairs, (int)top, (int)experts},
+      as_stream(stream)));
+}
+
+int qgemm_expert_combine(int dtype, const void* y, const int32_t* places, const float* gates,
+                         void* out, int64_t rows, int64_t tokens, int64_t top, int64_t N,
+                         void* stream) {
+  if (dtype != QGEMM_F16 && dtype != QGEMM_BF16) return QGEMM_ERR_FORMAT;
+  if (!below(rows, 0, kMaxIndex) || !below(tokens, 0, kMaxIndex) || !below(top, 0, kMaxIndex) ||
+      !below(N, 0, kMaxIndex) || rows * N >= kMaxIndex || tokens * N >= kMaxIndex ||
+      tokens * top >= kMaxIndex)
+    return QGEMM_ERR_SHAPE;
+  if (!present(y, rows * N) || !present(places, tokens * top) || !present(gates, tokens * top) ||
+      !present(out, tokens * N))
+    return QGEMM_ERR_NULL;
+  if (!aligned(y, 16) || !aligned(out, 16) || !aligned(places, 4) || !aligned(gates, 4))
+    return QGEMM_ERR_ALIGN;
+  int st = check_apart({{out, 2 * tokens * N}},
+                       {{y, 2 * rows * N}, {places, 4 * tokens * top}, {gates, 4 * tokens * top}});
+  if (st != QGEMM_OK) return st;
+  if (tokens == 0 || N == 0) return QGEMM_OK;
+  if ((st = check_device()) != QGEMM_OK) return st;
+  return launched(qgemm::launch_expert_combine(
+      dtype,
+      qgemm::ExpertCombine{static_cast<const uint16_t*>(y), places, gates, static_cast<uint16_t*>(out),
+                           rows, tokens, N, (int)top},
+      as_stream(stream)));
 }
 
 int qgemm_read_probe(const void* buf, int64_t bytes, uint32_t* sink, int64_t workgroups,

@@ -253,6 +253,70 @@ int64_t paged_attention_workspace(int64_t batch, int64_t heads, int64_t kv_heads
 hipError_t launch_paged_attention(int dtype, int cache_dtype, const PagedAttention& a,
                                   hipStream_t stream);
 
+// ---- int8 x int8 products, dense and by expert (w8a8.hip, experts.hip) -------
+
+// Rows of K elements (1 fp16, 2 bf16, 4 fp32), row_stride elements apart.
+hipError_t launch_quantize_int8(int dtype, const void* x, int64_t row_stride, int8_t* codes,
+                                float* scale, int64_t rows, int64_t K, hipStream_t stream);
+
+// Packed int8 weight of one expert: the FP8 tiles of 16 columns x 128 K (2 KB;
+// lane l holds k = kt*128 + 32 (l >> 4) + [0, 32) of column l & 15, bytes 16h +
+// [0, 16) of it at offset 1024h + 16l), zero where k >= K or the column is past
+// the last.  A gated weight of N = 2F columns alternates 16 columns of the first
+// half with the 16 of the second that they meet, so that one lane of a matrix
+// instruction ends up with both; each half is padded on its own.
+struct W8a8Geom {
+  int64_t cg, kt;   // column groups of 16 and K tiles of 128
+  int64_t bytes;    // of one expert
+};
+inline W8a8Geom w8a8_geom(int64_t K, int64_t N, bool gated) {
+  W8a8Geom g;
+  g.cg = gated ? 2 * cdiv(N / 2, kTileN) : cdiv(N, kTileN);
+  g.kt = cdiv(K, kTileK8);
+  g.bytes = g.cg * g.kt * kTileBytes;
+  return g;
+}
+hipError_t launch_prepack_w8a8(const int8_t* w, void* packed, int64_t experts, int64_t K, int64_t N,
+                               bool gated, hipStream_t stream);
+
+// offsets == nullptr: one weight for all M rows.  Otherwise rows offsets[e] ..
+// offsets[e + 1] - 1 take expert e's; row m reads row rows[m] of a (rows ==
+// nullptr: row m).
+struct W8a8 {
+  const int8_t* a;
+  const float* a_scale;
+  const uint8_t* w;
+  const float* w_scale;
+  const int32_t *offsets, *rows;
+  uint16_t* out;
+  int64_t a_rows, M, N, K, experts;
+  bool gated, bf16;
+};
+hipError_t launch_w8a8(const W8a8& p, hipStream_t stream);
+
+constexpr int kMaxExperts = 1024;
+constexpr int64_t kMaxPairs = (int64_t)1 << 22;
+struct ExpertPlan {
+  const void* ids;
+  bool wide;         // int64 ids, else int32
+  int32_t *offsets, *rows, *places;
+  int32_t* counts;   // workspace
+  int64_t pairs;
+  int top, experts;
+};
+int64_t expert_plan_workspace(int64_t pairs, int64_t experts);
+hipError_t launch_expert_plan(const ExpertPlan& p, hipStream_t stream);
+
+struct ExpertCombine {
+  const uint16_t* y;
+  const int32_t* places;
+  const float* gates;
+  uint16_t* out;
+  int64_t rows, tokens, N;
+  int top;
+};
+hipError_t launch_expert_combine(int dtype, const ExpertCombine& p, hipStream_t stream);
+
 // Streaming read of `bytes` bytes (a multiple of 16, buf 16-byte aligned) by
 // `workgroups` workgroups; one word per workgroup goes to sink.
 hipError_t launch_read_probe(const void* buf, int64_t bytes, uint32_t* sink, int64_t workgroups,

@@ -1,5 +1,5 @@
-// Quantizers on the device: MXFP4 (E2M1 + one E8M0 per 32 elements) and
-// per-tensor e4m3fn.  Both are bit-exact restatements of integer rules, so the
+// Quantizers on the device: MXFP4 (E2M1 + one E8M0 per 32 elements), per-tensor
+// e4m3fn and per-row int8.  All are bit-exact restatements of integer rules, so the
 // device and any correct host implementation agree byte for byte.
 #include "qgemm_common.h"
 
@@ -178,7 +178,77 @@ __global__ __launch_bounds__(256) void fp8_cast_partials_kernel(
   }
 }
 
+// ---------------------------------------------------------------------------
+// int8 by rows: scale = max(fp32(amax / 127), 2^-126), code = the nearest whole
+// number (even at ties) to fp32(x / scale); a row with an infinity or a NaN has
+// the scale NaN and codes of 0.
+// ---------------------------------------------------------------------------
+template <int DT>
+__device__ __forceinline__ void load8(float (&v)[8], const void* x, int64_t at) {
+  if constexpr (DT == 4) {
+    const floatx4* src = reinterpret_cast<const floatx4*>(static_cast<const float*>(x) + at);
+    const floatx4 a = src[0], b = src[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+  } else {
+    const uintx4 d = *reinterpret_cast<const uintx4*>(static_cast<const uint16_t*>(x) + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint16_t h = (uint16_t)(d[j >> 1] >> (16 * (j & 1)));
+      v[j] = DT == 1 ? (float)__builtin_bit_cast(_Float16, h)
+                     : __builtin_bit_cast(float, (uint32_t)h << 16);
+    }
+  }
+}
+
+// One workgroup a row, read twice: the largest magnitude (as bits: an infinity
+// or NaN is above every finite value), then the codes.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_int8_kernel(const void* __restrict__ x,
+                                                            int64_t row_stride,
+                                                            int8_t* __restrict__ codes,
+                                                            float* __restrict__ scale, int K) {
+  __shared__ uint32_t part[4];
+  const int64_t row = blockIdx.x;
+  uint32_t top = 0;
+  float v[8];
+  for (int k = 8 * threadIdx.x; k < K; k += 2048) {
+    load8<DT>(v, x, row * row_stride + k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = max(max(part[0], part[1]), max(part[2], part[3]));
+  const bool finite = top < 0x7f800000u;
+  const float s = finite ? fmaxf(__builtin_bit_cast(float, top) / 127.0f, 0x1p-126f)
+                         : __builtin_bit_cast(float, 0x7fc00000u);
+  if (threadIdx.x == 0) scale[row] = s;
+  for (int k = 8 * threadIdx.x; k < K; k += 2048) {
+    load8<DT>(v, x, row * row_stride + k);
+    uintx2 w = {0, 0};
+    if (finite) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j >> 2] |= (uint32_t)((int)__builtin_rintf(v[j] / s) & 255) << (8 * (j & 3));
+    }
+    *reinterpret_cast<uintx2*>(codes + row * K + k) = w;
+  }
+}
+
 }  // namespace
+
+hipError_t launch_quantize_int8(int dtype, const void* x, int64_t row_stride, int8_t* codes,
+                                float* scale, int64_t rows, int64_t K, hipStream_t stream) {
+  auto kernel = dtype == 1   ? quantize_int8_kernel<1>
+                : dtype == 2 ? quantize_int8_kernel<2>
+                             : quantize_int8_kernel<4>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(256), 0, stream, x, row_stride, codes, scale,
+                     (int)K);
+  return hipGetLastError();
+}
 
 hipError_t launch_quantize_fp8_ws(const float* x, int64_t count, uint8_t* codes, float* scale,
                                   float* partials, hipStream_t stream) {

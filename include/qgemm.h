@@ -12,8 +12,10 @@
  * (qgemm_w4a16_grouped, qgemm_w8a16_grouped), NVFP4 weights with fp16
  * activations (qgemm_nvfp4), and MXFP4 / FP8 GEMMs that quantize fp32
  * activations on the device inside the call (qgemm_mxfp4_act,
- * qgemm_fp8_act).  Next to them, the paged key-value cache of a decode step:
- * qgemm_kv_plan, qgemm_kv_append and qgemm_paged_attention.
+ * qgemm_fp8_act).  Products of 8-bit integers on both sides (qgemm_w8a8), also
+ * for rows grouped by expert (qgemm_w8a8_experts) with the routing around them.
+ * Next to them, the paged key-value cache of a decode step: qgemm_kv_plan,
+ * qgemm_kv_append and qgemm_paged_attention.
  *
  * Sources (short names):
  *   W4A16 page -- "Triton W4A16 blocked GEMM and Blackwell NVFP4"
@@ -83,7 +85,7 @@ enum qgemm_status {
   QGEMM_ERR_TOO_LARGE = -8, /* the input exceeds an entry point's fixed
                                scratch (qgemm_fp8_act_noalloc)              */
   QGEMM_ERR_OVERLAP = -9  /* buffers share memory that must not
-                             (qgemm_kv_plan)                                */
+                             (qgemm_kv_plan, the int8 and expert calls)     */
 };
 
 /* Human-readable text for a status code (static storage, never NULL). */
@@ -108,7 +110,8 @@ enum qgemm_kernel {
  * applies (the W8A16 page's performance and autotune notes and the FP8
  * page's parameter list choose a tile configuration per M, N, K; here a
  * fixed rule fitted to measurements does).  qgemm_mxfp4_act and
- * qgemm_fp8_act(_noalloc) dispatch as QGEMM_MXFP4 and QGEMM_FP8.  group_k is
+ * qgemm_fp8_act(_noalloc) dispatch as QGEMM_MXFP4 and QGEMM_FP8 (the int8 by
+ * int8 products, qgemm_w8a8, are not among them).  group_k is
  * read for the grouped formats only.  Host-only: touches no device.  Returns
  * a qgemm_kernel value, or a negative status for a format or sizes the entry
  * point would reject (QGEMM_ERR_FORMAT, QGEMM_ERR_SHAPE).
@@ -342,7 +345,8 @@ int qgemm_w8a16_grouped(const void* x, const void* w_packed, void* y, int64_t M,
 enum qgemm_dtype {
   QGEMM_F16 = 1,
   QGEMM_BF16 = 2,
-  QGEMM_E4M3 = 3          /* e4m3fn codes: caches only                       */
+  QGEMM_E4M3 = 3,         /* e4m3fn codes: caches only                       */
+  QGEMM_F32 = 4           /* qgemm_quantize_int8's input only                */
 };
 
 /*
@@ -431,6 +435,109 @@ int qgemm_paged_attention(int dtype, int cache_dtype, const void* q, const void*
                           int64_t head_stride, int64_t token_stride, int64_t width,
                           int64_t table_stride, int64_t max_len, int64_t window, float scale,
                           void* stream);
+
+/*
+ * Products of 8-bit integers with scales for each token and channel, for one
+ * weight or for rows grouped by expert.
+ *
+ * A mixture-of-experts layer runs, on one stream and without a copy to the host,
+ *   qgemm_quantize_int8   the tokens' activations to codes
+ *   qgemm_expert_plan     rows in the order of the experts, from the router's choice
+ *   qgemm_w8a8_experts    gated: each row's token gathered, gate and up projections
+ *   qgemm_quantize_int8   the rows' activations to codes
+ *   qgemm_w8a8_experts    the rows as they lie, down projection
+ *   qgemm_expert_combine  each token's rows summed with its gates
+ * and a dense layer the quantizer and qgemm_w8a8.
+ *
+ * Differing from the conventions above: fp32 and int32 arrays need 4-byte and
+ * int64 arrays 8-byte alignment only, and an output that shares memory with an
+ * input or another output is refused (QGEMM_ERR_OVERLAP).  K is a multiple of
+ * 16 and at most 131056, so that a sum of K products of two codes fits 32 bits;
+ * experts is 1 .. 1024.
+ */
+
+/*
+ * qgemm_quantize_int8 -- x: dtype (QGEMM_F16, QGEMM_BF16 or QGEMM_F32) [rows, K],
+ * row_stride elements between rows (a multiple of 16 bytes).  For each row
+ *   scale[r]    = max(fp32(max_k |x[r, k]| / 127), 2^-126)
+ *   codes[r, k] = fp32(x[r, k] / scale[r]) to the nearest whole number, even at ties,
+ * so codes are within +-127.  A row that holds an infinity or a NaN gets the scale
+ * NaN and codes of 0: its rows of a product are NaN.
+ */
+int qgemm_quantize_int8(int dtype, const void* x, int8_t* codes, float* scale, int64_t rows,
+                        int64_t K, int64_t row_stride, void* stream);
+
+/*
+ * qgemm_prepack_w8a8 -- pack int8 weights w [experts, K, N] for qgemm_w8a8
+ * (experts = 1) and qgemm_w8a8_experts.  gated is 0, or 1 for a weight whose
+ * columns are two halves, gate and up (N even).  w_packed holds
+ * qgemm_prepack_w8a8_bytes(...) bytes, all of which are written; one expert's
+ * share, of N rounded up to a multiple of 16 (each half, if gated) and K to one
+ * of 128, is below 2^31 bytes.
+ */
+int64_t qgemm_prepack_w8a8_bytes(int64_t experts, int64_t K, int64_t N, int gated);
+int qgemm_prepack_w8a8(const int8_t* w, void* w_packed, int64_t experts, int64_t K, int64_t N,
+                       int gated, void* stream);
+
+/*
+ * qgemm_w8a8 -- with Y[m, n] = (sum_k A[m, k] W[k, n]) * a_scale[m] * w_scale[n]:
+ *   gated = 0: out[m, n] = Y[m, n], out [M, N]
+ *   gated = 1: out[m, f] = silu(Y[m, f]) * Y[m, N/2 + f], out [M, N/2], with
+ *              silu(y) = y / (1 + exp(-y))
+ * a: int8 [M, K], any codes; a_scale fp32 [M]; w_packed from qgemm_prepack_w8a8
+ * with the same K, N and gated; w_scale fp32 [N]; out: dtype (QGEMM_F16 or
+ * QGEMM_BF16).  The sum is exact; it is rounded to fp32, multiplied by a_scale
+ * and then by w_scale in fp32, and the result is rounded once.  M * K and M * N
+ * are below 2^31.
+ */
+int qgemm_w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
+               const float* w_scale, void* out, int64_t M, int64_t N, int64_t K, int gated,
+               void* stream);
+
+/*
+ * qgemm_w8a8_experts -- qgemm_w8a8 with a weight for each stretch of rows: row m
+ * of the M rows of out, offsets[e] <= m < offsets[e + 1], takes W[e] and
+ * w_scale[e] ([experts, N]).  offsets int32 [experts + 1] on the device must not
+ * fall; they are held to 0 .. M, rows before the first and from the last on are
+ * left as they were, and an expert may have no rows.  (Where offsets fall, rows
+ * of out are unspecified.)  rows NULL: row m reads row m of a and a_scale, and
+ * a_rows is M.  Otherwise rows int32 [M] names the row, 0 .. a_rows - 1, that
+ * each reads; one outside gives a row of zeros.  a_rows * K is below 2^31.
+ */
+int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
+                       const float* w_scale, const int32_t* offsets, const int32_t* rows, void* out,
+                       int64_t a_rows, int64_t M, int64_t N, int64_t K, int64_t experts, int gated,
+                       void* stream);
+
+/*
+ * qgemm_expert_plan -- the order of a batch's rows.  ids [tokens, top] (int32 or
+ * int64: id_bytes 4 or 8) are the experts that each token goes to; an id below 0
+ * or at or above experts has no row (an expert that another GPU holds).  The
+ * other pairs (token, choice) are sorted by expert, within an expert in their own
+ * order:
+ *   offsets [experts + 1]  offsets[e]: pairs of the experts before e
+ *   rows [tokens * top]    token of each sorted row; -1 from offsets[experts] on
+ *   places [tokens, top]   sorted row of each pair; -1 where it has none
+ * all int32.  tokens * top is at most 2^22.  workspace:
+ * qgemm_expert_plan_workspace_bytes(...) bytes, 16-byte aligned, of any contents;
+ * calls that share one must not overlap.  May be NULL where that size is 0.
+ */
+int64_t qgemm_expert_plan_workspace_bytes(int64_t tokens, int64_t top, int64_t experts);
+int qgemm_expert_plan(int id_bytes, const void* ids, int32_t* offsets, int32_t* rows,
+                      int32_t* places, void* workspace, int64_t tokens, int64_t top,
+                      int64_t experts, void* stream);
+
+/*
+ * qgemm_expert_combine -- out[t, n] = sum_j gates[t, j] * y[places[t, j], n] over
+ * the choices j = 0 .. top - 1, in that order, in fp32, rounded once.  y: dtype
+ * (QGEMM_F16 or QGEMM_BF16) [rows, N]; places int32 and gates fp32 [tokens, top];
+ * out dtype [tokens, N].  A place below 0 or at or above rows is left out,
+ * whatever its gate; a token without any gets zeros.  rows * N, tokens * N and
+ * tokens * top are below 2^31.
+ */
+int qgemm_expert_combine(int dtype, const void* y, const int32_t* places, const float* gates,
+                         void* out, int64_t rows, int64_t tokens, int64_t top, int64_t N,
+                         void* stream);
 
 /*
  * qgemm_read_probe -- measurement reference, not part of any GEMM: reads the

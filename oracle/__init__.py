@@ -20,7 +20,8 @@ Sources (the web pages these functions restate; short names used below):
 Group-wise scales and zero points (grouped.py) follow the W4A16 page's
 section 1 dequant form and the W8A16 page's extensions; NVFP4-style two-level
 block scaling (nvfp4.py) the W4A16 page's section 3.  The paged key-value cache
-(kvcache.py) is written from its formulas.
+(kvcache.py) and the int8 products, dense and by expert (int8.py), are written
+from their formulas.
 
 Parity status of each function is stated in its module.  Parity unpinned:
 the FP8 per-tensor scale formula (the FP8 page fixes only the 448 range and
@@ -51,6 +52,13 @@ from .grouped import (
     gemm_w8a16_grouped,
 )
 from .kvcache import kv_plan, kv_append, paged_attention
+from .int8 import (
+    quantize_int8,
+    gemm_w8a8,
+    gemm_w8a8_experts,
+    expert_plan,
+    expert_combine,
+)
 from .gemm import (
     dequant_w4,
     dequant_w8,
@@ -96,4 +104,9 @@ __all__ = [
     "kv_plan",
     "kv_append",
     "paged_attention",
+    "quantize_int8",
+    "gemm_w8a8",
+    "gemm_w8a8_experts",
+    "expert_plan",
+    "expert_combine",
 ]

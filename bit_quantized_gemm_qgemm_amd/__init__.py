@@ -71,7 +71,7 @@ _SIGNATURES = [
      [ctypes.c_int] + [_P] * 5 + [_I64] * 3 + [ctypes.c_int, _P]),
     ("qgemm_w8a8_experts", ctypes.c_int,
      [ctypes.c_int] + [_P] * 7 + [_I64] * 5 + [ctypes.c_int, _P]),
-    ("qgemm_expert_plan_workspace_bytes", ctypes.c_int64, [_I64] * 3),
+    ("qgemm_expert_plan_workspace_bytes", ctypes.c_int64, [_I64] * 2),
     ("qgemm_expert_plan", ctypes.c_int, [ctypes.c_int] + [_P] * 5 + [_I64] * 3 + [_P]),
     ("qgemm_expert_combine", ctypes.c_int, [ctypes.c_int] + [_P] * 4 + [_I64] * 4 + [_P]),
     ("qgemm_read_probe", ctypes.c_int, [_P, _I64, _P, _I64, _P]),
@@ -824,8 +824,8 @@ def qgemm_w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows=None, gat
     return out
 
 
-def qgemm_expert_plan_workspace_bytes(tokens, top, experts):
-    n = lib().qgemm_expert_plan_workspace_bytes(int(tokens), int(top), int(experts))
+def qgemm_expert_plan_workspace_bytes(pairs, experts):
+    n = lib().qgemm_expert_plan_workspace_bytes(int(pairs), int(experts))
     if n < 0:
         raise QgemmError(int(n), "qgemm_expert_plan_workspace_bytes")
     return int(n)
@@ -840,13 +840,13 @@ def qgemm_expert_plan(ids, experts, out=None, workspace=None):
     in their own order within one; rows[m] is the token of row m (-1 from
     offsets[-1] on), places[t, j] the row of a token's choice (-1: none).
     `out` may be a tuple of those three to write into; workspace: uint8, at least
-    qgemm_expert_plan_workspace_bytes(tokens, top, experts), allocated if None."""
+    qgemm_expert_plan_workspace_bytes(tokens * top, experts), allocated if None."""
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch tensor")
     device, experts = ids.get_device(), int(experts)
     _dense(ids, _ID_BYTES, 2, "ids", device)
     tokens, top = ids.shape
-    need = qgemm_expert_plan_workspace_bytes(tokens, top, experts)
+    need = qgemm_expert_plan_workspace_bytes(tokens * top, experts)
     if out is None:
         i32 = {"dtype": torch.int32, "device": ids.device}
         out = (torch.empty(experts + 1, **i32), torch.empty(tokens * top, **i32),

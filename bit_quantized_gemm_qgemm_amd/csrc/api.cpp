@@ -861,20 +861,20 @@ int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const v
               stream);
 }
 
-int64_t qgemm_expert_plan_workspace_bytes(int64_t tokens, int64_t top, int64_t experts) {
-  if (!below(tokens, 0, kMaxIndex) || !below(top, 0, kMaxIndex) ||
-      !below(experts, 1, qgemm::kMaxExperts + 1) || tokens * top > qgemm::kMaxPairs)
+int64_t qgemm_expert_plan_workspace_bytes(int64_t pairs, int64_t experts) {
+  if (!below(pairs, 0, qgemm::kMaxPairs + 1) || !below(experts, 1, qgemm::kMaxExperts + 1))
     return QGEMM_ERR_SHAPE;
-  return qgemm::expert_plan_workspace(tokens * top, experts);
+  return qgemm::expert_plan_workspace(pairs, experts);
 }
 
 int qgemm_expert_plan(int id_bytes, const void* ids, int32_t* offsets, int32_t* rows,
                       int32_t* places, void* workspace, int64_t tokens, int64_t top,
                       int64_t experts, void* stream) {
   if (id_bytes != 4 && id_bytes != 8) return QGEMM_ERR_FORMAT;
-  const int64_t need = qgemm_expert_plan_workspace_bytes(tokens, top, experts);
-  if (need < 0) return (int)need;
+  if (!below(tokens, 0, kMaxIndex) || !below(top, 0, kMaxIndex)) return QGEMM_ERR_SHAPE;
   const int64_t pairs = tokens * top;
+  const int64_t need = qgemm_expert_plan_workspace_bytes(pairs, experts);
+  if (need < 0) return (int)need;
   if (!present(ids, pairs) || !offsets || !present(rows, pairs) || !present(places, pairs) ||
       !present(workspace, need))
     return QGEMM_ERR_NULL;

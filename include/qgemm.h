@@ -519,10 +519,10 @@ int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const v
  *   rows [tokens * top]    token of each sorted row; -1 from offsets[experts] on
  *   places [tokens, top]   sorted row of each pair; -1 where it has none
  * all int32.  tokens * top is at most 2^22.  workspace:
- * qgemm_expert_plan_workspace_bytes(...) bytes, 16-byte aligned, of any contents;
+ * qgemm_expert_plan_workspace_bytes(tokens * top, experts) bytes, 16-byte aligned, of any contents;
  * calls that share one must not overlap.  May be NULL where that size is 0.
  */
-int64_t qgemm_expert_plan_workspace_bytes(int64_t tokens, int64_t top, int64_t experts);
+int64_t qgemm_expert_plan_workspace_bytes(int64_t pairs, int64_t experts);
 int qgemm_expert_plan(int id_bytes, const void* ids, int32_t* offsets, int32_t* rows,
                       int32_t* places, void* workspace, int64_t tokens, int64_t top,
                       int64_t experts, void* stream);

@@ -69,7 +69,7 @@ def test_plan_in_a_graph_follows_its_ids():
     rng = np.random.default_rng(3)
     T, top, experts = 3000, 4, 100
     ids = dev(rng.integers(0, experts, (T, top)))
-    ws = torch.empty(qg.qgemm_expert_plan_workspace_bytes(T, top, experts), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(qg.qgemm_expert_plan_workspace_bytes(T * top, experts), dtype=torch.uint8, device="cuda")
     out = qg.qgemm_expert_plan(ids, experts, workspace=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()

@@ -71,6 +71,7 @@ _SIGNATURES = [
      [ctypes.c_int] + [_P] * 5 + [_I64] * 3 + [ctypes.c_int, _P]),
     ("qgemm_w8a8_experts", ctypes.c_int,
      [ctypes.c_int] + [_P] * 7 + [_I64] * 5 + [ctypes.c_int, _P]),
+    ("qgemm_w8a8_tile", ctypes.c_int, [_I64] * 4 + [ctypes.c_int] + [_P] * 3),
     ("qgemm_expert_plan_workspace_bytes", ctypes.c_int64, [_I64] * 2),
     ("qgemm_expert_plan", ctypes.c_int, [ctypes.c_int] + [_P] * 5 + [_I64] * 3 + [_P]),
     ("qgemm_expert_combine", ctypes.c_int, [ctypes.c_int] + [_P] * 4 + [_I64] * 4 + [_P]),
@@ -822,6 +823,15 @@ def qgemm_w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows=None, gat
             None if rows is None else rows.data_ptr(), out.data_ptr(), a_rows, M, N, K, experts,
             int(gated), _stream(a))
     return out
+
+
+def qgemm_w8a8_tile(M, N, K, experts=0, gated=False):
+    """(rows, columns, parts of K) of a workgroup of qgemm_w8a8, or with
+    experts > 0 of qgemm_w8a8_experts, with these sizes; host-only."""
+    out = [_I64(), _I64(), _I64()]
+    _check(lib().qgemm_w8a8_tile(int(M), int(N), int(K), int(experts), int(gated),
+                                 *(ctypes.addressof(x) for x in out)), "qgemm_w8a8_tile")
+    return tuple(x.value for x in out)
 
 
 def qgemm_expert_plan_workspace_bytes(pairs, experts):

@@ -861,6 +861,27 @@ int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const v
               stream);
 }
 
+int qgemm_w8a8_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int gated, int64_t* rows,
+                    int64_t* cols, int64_t* k_split) {
+  const int st = check_w8a8_weight(experts == 0 ? 1 : experts, K, N, gated);
+  if (st != QGEMM_OK) return st;
+  if (!below(M, 0, kMaxIndex) || M * N >= kMaxIndex) return QGEMM_ERR_SHAPE;
+  if (!rows || !cols || !k_split) return QGEMM_ERR_NULL;
+  static const int32_t some = 0;
+  qgemm::W8a8 p{};
+  p.offsets = experts == 0 ? nullptr : &some;   // not read
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.experts = experts == 0 ? 1 : experts;
+  p.gated = gated != 0;
+  const qgemm::W8a8Tile t = qgemm::w8a8_tile(p);
+  *rows = t.rows;
+  *cols = t.cols;
+  *k_split = t.k_split;
+  return QGEMM_OK;
+}
+
 int64_t qgemm_expert_plan_workspace_bytes(int64_t pairs, int64_t experts) {
   if (!below(pairs, 0, qgemm::kMaxPairs + 1) || !below(experts, 1, qgemm::kMaxExperts + 1))
     return QGEMM_ERR_SHAPE;

@@ -293,6 +293,12 @@ struct W8a8 {
   bool gated, bf16;
 };
 hipError_t launch_w8a8(const W8a8& p, hipStream_t stream);
+// The workgroups' tile that it takes (sizes, offsets set or not, gated): rows,
+// columns, waves that share K.
+struct W8a8Tile {
+  int rows, cols, k_split;
+};
+W8a8Tile w8a8_tile(const W8a8& p);
 
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxPairs = (int64_t)1 << 22;

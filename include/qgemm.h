@@ -110,8 +110,8 @@ enum qgemm_kernel {
  * applies (the W8A16 page's performance and autotune notes and the FP8
  * page's parameter list choose a tile configuration per M, N, K; here a
  * fixed rule fitted to measurements does).  qgemm_mxfp4_act and
- * qgemm_fp8_act(_noalloc) dispatch as QGEMM_MXFP4 and QGEMM_FP8 (the int8 by
- * int8 products, qgemm_w8a8, are not among them).  group_k is
+ * qgemm_fp8_act(_noalloc) dispatch as QGEMM_MXFP4 and QGEMM_FP8 (for the int8 by
+ * int8 products see qgemm_w8a8_tile).  group_k is
  * read for the grouped formats only.  Host-only: touches no device.  Returns
  * a qgemm_kernel value, or a negative status for a format or sizes the entry
  * point would reject (QGEMM_ERR_FORMAT, QGEMM_ERR_SHAPE).
@@ -508,6 +508,15 @@ int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const v
                        const float* w_scale, const int32_t* offsets, const int32_t* rows, void* out,
                        int64_t a_rows, int64_t M, int64_t N, int64_t K, int64_t experts, int gated,
                        void* stream);
+
+/*
+ * qgemm_w8a8_tile -- how the int8 products share their work with these sizes: a
+ * workgroup takes *rows x *cols of the product (N columns), its waves K in
+ * *k_split parts.  experts 0 asks for qgemm_w8a8, 1 .. 1024 for
+ * qgemm_w8a8_experts.  Host-only: touches no device.
+ */
+int qgemm_w8a8_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int gated, int64_t* rows,
+                    int64_t* cols, int64_t* k_split);
 
 /*
  * qgemm_expert_plan -- the order of a batch's rows.  ids [tokens, top] (int32 or

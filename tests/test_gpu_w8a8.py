@@ -78,6 +78,34 @@ def test_dense_of_ordinary_sizes_and_odd_columns(M, K, N):
     dense(M, K, N, False, torch.bfloat16)
 
 
+TILES = [(16, 16, 8), (16, 32, 4), (16, 64, 4), (32, 32, 4), (32, 64, 4), (32, 128, 1), (64, 64, 2), (64, 128, 1),
+         (96, 256, 1), (128, 128, 1), (128, 256, 1), (256, 256, 1)]
+
+
+def sizes_of(tile, experts, most):
+    """Sizes that take this tile, the cheapest of a grid first, with K tiles of every remainder."""
+    found = []
+    for M in (1, 17, 70, 129, 200, 300, 385, 513, 700, 1000, 1500, 2049):
+        for N in (34, 130, 258, 642, 1282, 2050, 4098, 8194):
+            for K in (16, 272, 400, 528, 1040, 2064, 4112):
+                if M * N * K <= 1.25e10 and qg.qgemm_w8a8_tile(M, N, K, experts) == tile:
+                    found.append((M * N * K + 3 * K * N * max(1, experts) + 20 * M * N, M, N, K))
+    out = []
+    for _, M, N, K in sorted(found)[:most]:
+        out += [(M, N, k) for k in (K, K + 128, K + 256, K + 400)
+                if qg.qgemm_w8a8_tile(M, N, k, experts) == tile]
+    return out
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_dense_of_each_tile(tile):
+    sizes = sizes_of(tile, 0, 2)
+    assert sizes
+    for i, (M, N, K) in enumerate(sizes):
+        print("tile", tile, flush=True)
+        dense(M, K, N, gated=i % 2 == 1 and tile != (16, 16, 8), dtype=list(HALF)[i % 2])
+
+
 def test_dense_without_k_rows_or_columns():
     print("case w8a8 empty", flush=True)
     f32 = lambda *s: torch.ones(s, device="cuda")
@@ -179,6 +207,19 @@ def test_experts_leave_rows_outside_as_they_were():
         experts_case([5, 0, 21], 256, 66, False, torch.bfloat16, gather, lead=3, tail=14)
         experts_case([0, 0], 256, 66, True, torch.float16, gather, lead=2, tail=5)
         experts_case([150, 0, 90], 256, 66, True, torch.float16, gather, lead=2, tail=300)
+
+
+@pytest.mark.parametrize("tile", TILES[:-1])    # the largest is for single weights
+def test_experts_of_each_tile(tile):
+    sizes = sizes_of(tile, 3, 1) + sizes_of(tile, 20, 1)
+    assert sizes
+    rng = np.random.default_rng(5)
+    for i, (M, N, K) in enumerate(sizes):
+        experts = 3 if qg.qgemm_w8a8_tile(M, N, K, 3) == tile else 20
+        cuts = np.sort(rng.integers(0, M + 1, experts - 1))
+        counts = np.diff(np.concatenate([[0], cuts, [M]]))
+        print("tile", tile, flush=True)
+        experts_case(list(counts), K, N, i % 2 == 1 and tile != (16, 16, 8), list(HALF)[i % 2], i % 3 != 1)
 
 
 @pytest.mark.parametrize("experts", [63, 64, 65, 127, 128, 257, 1024])

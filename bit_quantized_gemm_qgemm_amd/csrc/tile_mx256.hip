@@ -344,7 +344,9 @@ __global__ __launch_bounds__(256) void mxw_kernel(const uint8_t* __restrict__ a,
     mxw_copies<2>(cst, s, P);
     mxw_copies<3>(cst, s, P);
   }
-  QG_WAIT_VM_BARRIER(20);   // the W loads and step 0's copies landed
+  // the W loads and the copies of steps 0 and 1 landed: in step 0 only 27 instructions
+  // follow those of step 1, fewer than the wait there counts on (39)
+  QG_WAIT_VM_BARRIER(10);
   uintx4 x[2][8];
   uint32_t sa[WB][8];
   mxw_read_a<0>(x[0], smem, P);
@@ -634,7 +636,9 @@ __global__ __launch_bounds__(256) void f8w_kernel(const uint8_t* __restrict__ a,
     f8w_copies<2>(cst, s, wave, P);
     f8w_copies<3>(cst, s, wave, P);
   }
-  QG_WAIT_VM_BARRIER(16);   // B and step 0's copies landed
+  // B and the copies of steps 0 and 1 landed: in step 0 only 20 instructions follow
+  // those of step 1, fewer than the wait there counts on (28)
+  QG_WAIT_VM_BARRIER(8);
   uintx4 x[2][4][2];
   f8w_read_a<0>(x[0], smem, P);
   // nothing of the lgkm counter left pending on the way into the loop (the

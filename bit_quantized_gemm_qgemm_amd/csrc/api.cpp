@@ -935,7 +935,7 @@ int qgemm_expert_combine(int dtype, const void* y, const int32_t* places, const 
   return launched(qgemm::launch_expert_combine(
       dtype,
       qgemm::ExpertCombine{static_cast<const uint16_t*>(y), places, gates, static_cast<uint16_t*>(out),
-                           rows, tokens, N, (int)top},
+                           (uint32_t)rows, (uint32_t)tokens, (uint32_t)N, (int)top},
       as_stream(stream)));
 }
 

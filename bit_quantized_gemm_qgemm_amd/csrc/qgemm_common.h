@@ -318,7 +318,7 @@ struct ExpertCombine {
   const int32_t* places;
   const float* gates;
   uint16_t* out;
-  int64_t rows, tokens, N;
+  uint32_t rows, tokens, N;
   int top;
 };
 hipError_t launch_expert_combine(int dtype, const ExpertCombine& p, hipStream_t stream);

@@ -183,71 +183,217 @@ __global__ __launch_bounds__(256) void fp8_cast_partials_kernel(
 // number (even at ties) to fp32(x / scale); a row with an infinity or a NaN has
 // the scale NaN and codes of 0.
 // ---------------------------------------------------------------------------
+// Eight elements of a row as they are stored (1 fp16, 2 bf16, 4 fp32).
 template <int DT>
-__device__ __forceinline__ void load8(float (&v)[8], const void* x, int64_t at) {
-  if constexpr (DT == 4) {
-    const floatx4* src = reinterpret_cast<const floatx4*>(static_cast<const float*>(x) + at);
-    const floatx4 a = src[0], b = src[1];
+struct Eight {
+  static constexpr int kWords = DT == 4 ? 8 : 4;
+  uint32_t d[kWords];
+
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    const uintx4* src = DT == 4
+        ? reinterpret_cast<const uintx4*>(static_cast<const float*>(x) + at)
+        : reinterpret_cast<const uintx4*>(static_cast<const uint16_t*>(x) + at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-  } else {
-    const uintx4 d = *reinterpret_cast<const uintx4*>(static_cast<const uint16_t*>(x) + at);
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uintx4 v = __builtin_nontemporal_load(src + i);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint16_t h = (uint16_t)(d[j >> 1] >> (16 * (j & 1)));
-      v[j] = DT == 1 ? (float)__builtin_bit_cast(_Float16, h)
-                     : __builtin_bit_cast(float, (uint32_t)h << 16);
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = v[j];
     }
+  }
+
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (DT == 4) return __builtin_bit_cast(float, d[j]);
+    const uint16_t h = (uint16_t)(d[j >> 1] >> (16 * (j & 1)));
+    return DT == 1 ? (float)__builtin_bit_cast(_Float16, h) : __builtin_bit_cast(float, (uint32_t)h << 16);
+  }
+};
+
+// Largest magnitudes as bits, which order as the values do and hold an infinity
+// or a NaN above every finite one: a pair of 16-bit elements at a time.
+template <int DT>
+struct Largest {
+  typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+  uint32_t bits = 0;
+
+  __device__ __forceinline__ void take(uint32_t d) {
+    if constexpr (DT == 4)
+      bits = max(bits, d & 0x7fffffffu);
+    else
+      bits = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+          __builtin_bit_cast(ushort2_t, bits), __builtin_bit_cast(ushort2_t, d & 0x7fff7fffu)));
+  }
+  // of one element, as fp32 bits (a NaN or infinity stays one)
+  __device__ __forceinline__ uint32_t whole() const {
+    if constexpr (DT == 4) return bits;
+    const uint32_t h = max(bits & 0xffffu, bits >> 16);
+    if constexpr (DT == 2) return h << 16;
+    return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)h)) & 0x7fffffffu;
+  }
+};
+
+// Codes of x / s, rounded as the division and then to whole numbers.  With r the
+// rounded reciprocal, q = x r is within two steps of x / s; one fused correction by
+// the remainder x - q s brings it within one and a second, whose remainder is then
+// exact, rounds as the division would, unless a remainder underflows where a code
+// is not 0: below s = 2^-60 both are multiplied by 2^64 first, which is exact.
+// Adding 1.5 * 2^23 leaves the nearest whole number in the low bits.
+struct Coder {
+  float s, r, lift;
+  bool finite;
+  __device__ __forceinline__ explicit Coder(float scale) {
+    lift = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+    s = scale * lift;
+    r = 1.0f / s;
+    finite = scale == scale;
+  }
+  __device__ __forceinline__ uint32_t code(float x) const {
+    x *= lift;
+    float q = x * r;
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+    return __builtin_bit_cast(uint32_t, q + 12582912.0f);
+  }
+  template <int DT>
+  __device__ __forceinline__ uintx2 codes(const Eight<DT>& v) const {
+    uintx2 w = {0, 0};
+    if (!finite) return w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = code(v.at(4 * i + j));
+      // low bytes: of two each, then of four
+      const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
+      w[i] = lo | hi;
+    }
+    return w;
+  }
+};
+
+__device__ __forceinline__ float int8_scale(uint32_t top) {
+  return top < 0x7f800000u ? fmaxf(__builtin_bit_cast(float, top) / 127.0f, 0x1p-126f)
+                           : __builtin_bit_cast(float, 0x7fc00000u);
+}
+
+// WAVES waves share a row and keep it in registers, 8 ROUNDS elements a lane;
+// workgroups of 4 waves, or of 16.
+template <int DT, int WAVES, int ROUNDS>
+__global__ __launch_bounds__(WAVES > 4 ? 1024 : 256) void quantize_int8_kernel(
+    const void* __restrict__ x, int64_t row_stride, int8_t* __restrict__ codes,
+    float* __restrict__ scale, int64_t rows, int K) {
+  constexpr int kPerGroup = WAVES == 1 ? 4 : 1;   // rows of a workgroup
+  __shared__ uint32_t part[WAVES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = kPerGroup * (int64_t)blockIdx.x + (WAVES == 1 ? wave : 0);
+  if (row >= rows) return;   // a wave of its own
+  const int first = 8 * (WAVES == 1 ? lane : (int)threadIdx.x);
+  Eight<DT> v[ROUNDS];
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int k = first + 512 * WAVES * i;
+    if (k < K) {
+      v[i].load(x, row * row_stride + k);
+    } else {
+#pragma unroll
+      for (int j = 0; j < Eight<DT>::kWords; ++j) v[i].d[j] = 0;
+    }
+  }
+  Largest<DT> m;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i)
+#pragma unroll
+    for (int j = 0; j < Eight<DT>::kWords; ++j) m.take(v[i].d[j]);
+  uint32_t top = m.whole();
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  if constexpr (WAVES > 1) {
+    if (lane == 0) part[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = max(top, part[w]);
+  }
+  const float s = int8_scale(top);
+  if (first == 0) scale[row] = s;
+  const Coder coder(s);
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int k = first + 512 * WAVES * i;
+    if (k < K)
+      __builtin_nontemporal_store(coder.codes(v[i]), reinterpret_cast<uintx2*>(codes + row * K + k));
   }
 }
 
-// One workgroup a row, read twice: the largest magnitude (as bits: an infinity
-// or NaN is above every finite value), then the codes.
+// Longer rows are read twice, by 16 waves.
 template <int DT>
-__global__ __launch_bounds__(256) void quantize_int8_kernel(const void* __restrict__ x,
-                                                            int64_t row_stride,
-                                                            int8_t* __restrict__ codes,
-                                                            float* __restrict__ scale, int K) {
-  __shared__ uint32_t part[4];
+__global__ __launch_bounds__(1024) void quantize_int8_long_kernel(const void* __restrict__ x,
+                                                                  int64_t row_stride,
+                                                                  int8_t* __restrict__ codes,
+                                                                  float* __restrict__ scale, int K) {
+  __shared__ uint32_t part[16];
   const int64_t row = blockIdx.x;
-  uint32_t top = 0;
-  float v[8];
-  for (int k = 8 * threadIdx.x; k < K; k += 2048) {
-    load8<DT>(v, x, row * row_stride + k);
+  Largest<DT> m;
+  Eight<DT> v;
+  for (int k = 8 * threadIdx.x; k < K; k += 8192) {
+    v.load(x, row * row_stride + k);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
+    for (int j = 0; j < Eight<DT>::kWords; ++j) m.take(v.d[j]);
   }
+  uint32_t top = m.whole();
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
   __syncthreads();
-  top = max(max(part[0], part[1]), max(part[2], part[3]));
-  const bool finite = top < 0x7f800000u;
-  const float s = finite ? fmaxf(__builtin_bit_cast(float, top) / 127.0f, 0x1p-126f)
-                         : __builtin_bit_cast(float, 0x7fc00000u);
-  if (threadIdx.x == 0) scale[row] = s;
-  for (int k = 8 * threadIdx.x; k < K; k += 2048) {
-    load8<DT>(v, x, row * row_stride + k);
-    uintx2 w = {0, 0};
-    if (finite) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j >> 2] |= (uint32_t)((int)__builtin_rintf(v[j] / s) & 255) << (8 * (j & 3));
-    }
-    *reinterpret_cast<uintx2*>(codes + row * K + k) = w;
+  for (int w = 0; w < 16; ++w) top = max(top, part[w]);
+  const float s = int8_scale(top);
+  if (threadIdx.x == 0) scale[row] = s;
+  const Coder coder(s);
+  for (int k = 8 * threadIdx.x; k < K; k += 8192) {
+    v.load(x, row * row_stride + k);
+    *reinterpret_cast<uintx2*>(codes + row * K + k) = coder.codes(v);
   }
+}
+
+template <int DT, int WAVES, int ROUNDS>
+void quantize_rows(const void* x, int64_t row_stride, int8_t* codes, float* scale, int64_t rows, int K,
+                   hipStream_t stream) {
+  hipLaunchKernelGGL((quantize_int8_kernel<DT, WAVES, ROUNDS>),
+                     dim3((unsigned)cdiv(rows, WAVES == 1 ? 4 : 1)), dim3(WAVES > 4 ? 1024 : 256), 0,
+                     stream, x, row_stride, codes, scale, rows, K);
+}
+
+template <int DT>
+hipError_t quantize_int8(const void* x, int64_t row_stride, int8_t* codes, float* scale, int64_t rows,
+                         int K, hipStream_t stream) {
+  if (K <= 512)
+    quantize_rows<DT, 1, 1>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 1024)
+    quantize_rows<DT, 1, 2>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 2048)
+    quantize_rows<DT, 1, 4>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 4096)
+    quantize_rows<DT, 4, 2>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 8192)
+    quantize_rows<DT, 4, 4>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 16384)
+    quantize_rows<DT, 4, 8>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 32768)
+    quantize_rows<DT, 16, 4>(x, row_stride, codes, scale, rows, K, stream);
+  else if (K <= 65536)
+    quantize_rows<DT, 16, 8>(x, row_stride, codes, scale, rows, K, stream);
+  else
+    hipLaunchKernelGGL((quantize_int8_long_kernel<DT>), dim3((unsigned)rows), dim3(1024), 0, stream, x,
+                       row_stride, codes, scale, K);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_quantize_int8(int dtype, const void* x, int64_t row_stride, int8_t* codes,
                                 float* scale, int64_t rows, int64_t K, hipStream_t stream) {
-  auto kernel = dtype == 1   ? quantize_int8_kernel<1>
-                : dtype == 2 ? quantize_int8_kernel<2>
-                             : quantize_int8_kernel<4>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(256), 0, stream, x, row_stride, codes, scale,
-                     (int)K);
-  return hipGetLastError();
+  auto run = dtype == 1 ? quantize_int8<1> : dtype == 2 ? quantize_int8<2> : quantize_int8<4>;
+  return run(x, row_stride, codes, scale, rows, (int)K, stream);
 }
 
 hipError_t launch_quantize_fp8_ws(const float* x, int64_t count, uint8_t* codes, float* scale,

@@ -42,7 +42,7 @@ def plan_case(ids, experts, dtype=torch.int64):
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 @pytest.mark.parametrize("tokens,top,experts", [
     (1, 1, 1), (1, 8, 64), (7, 3, 5), (32, 8, 128), (64, 1, 2), (65, 2, 63), (100, 6, 64), (513, 4, 65),
-    (1000, 8, 256), (1024, 8, 257), (1025, 8, 60), (2049, 8, 1024), (5000, 5, 1000), (9000, 8, 16),
+    (1000, 8, 256), (1024, 8, 257), (1025, 8, 60), (2049, 8, 1024), (5000, 5, 1000), (9000, 8, 16), (600, 8, 300), (33000, 8, 20), (40000, 7, 1024),
 ])
 def test_plan_matches_the_oracle(tokens, top, experts, dtype):
     rng = np.random.default_rng(tokens + experts)

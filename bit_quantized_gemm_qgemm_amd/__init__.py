@@ -8,9 +8,10 @@ name on torch's current stream.  Every step of the computation runs in the
 library's HIP kernels; there is no fallback.  If libqgemm.so is missing the
 calls raise instead of computing anything.
 
-The key-value cache calls, made for every layer of a decode step, marshal their
-usual arguments in native code (the module _binding); what that does not take
-goes through the checks here, and everything where it is not built.
+The calls that a decode step makes for every layer (key-value cache, int8 and
+expert products) marshal their usual arguments in native code (the module
+_binding); what that does not take goes through the checks here, and everything
+where it is not built.
 """
 
 import ctypes
@@ -110,7 +111,7 @@ def lib():
         except ImportError as e:
             _binding = None
             warnings.warn(f"the native binding is not built for this interpreter ({e}); the "
-                          "key-value cache calls take 4 to 5 us longer.  Run "
+                          "calls of a decode step take 3 to 5 us longer.  Run "
                           "`python -m bit_quantized_gemm_qgemm_amd.build`", RuntimeWarning,
                           stacklevel=2)
         _lib, _native = handle, _binding
@@ -682,6 +683,8 @@ def qgemm_paged_attention(q, k_cache, v_cache, table, lens, k_scale=None, v_scal
 
 
 # ---- int8 x int8 products, dense and by expert ---------------------------------
+#
+# As above: a call that brings its outputs and workspace tries the native binding.
 
 _ROW_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 4}
 _INT8 = (torch.int8,)
@@ -715,6 +718,12 @@ def qgemm_quantize_int8(x, out=None):
     row, codes = x / scale to the nearest whole number.  A row with an infinity
     or a NaN gets the scale NaN and codes of 0.  `out` may be a tuple of those
     two tensors to write into."""
+    status = None
+    if _native and out is not None:
+        status = _native.quantize_int8(x, out)
+    if status is not None:
+        _check(status, "qgemm_quantize_int8")
+        return out
     (rows, K), (row_stride,) = _view(x, _ROW_TYPES, 2, "x")
     device = x.get_device()
     if out is None:
@@ -778,6 +787,12 @@ def qgemm_w8a8(a, a_scale, w_packed, w_scale, N, gated=False, dtype=torch.bfloat
     a: int8 [M, K] codes and a_scale float32 [M], as qgemm_quantize_int8 gives
     them; w_packed from qgemm_prepack_w8a8 with the same `gated`; w_scale
     float32 [N]."""
+    status = None
+    if _native and out is not None:
+        status = _native.w8a8(a, a_scale, w_packed, w_scale, N, gated, out)
+    if status is not None:
+        _check(status, "qgemm_w8a8")
+        return out
     N = int(N)
     device, M, K = _w8a8_operands(a, a_scale, w_packed, 1, N, gated)
     _dense(w_scale, _FLOAT32, 1, "w_scale", device)
@@ -801,6 +816,12 @@ def qgemm_w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows=None, gat
     [experts + 1].  rows, int32 [M], names the row of a (and a_scale) that each
     of the M output rows reads; without it row m reads row m.  Rows that no
     expert has are left as they were."""
+    status = None
+    if _native and out is not None:
+        status = _native.w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows, gated, out)
+    if status is not None:
+        _check(status, "qgemm_w8a8_experts")
+        return out
     N = int(N)
     if not isinstance(offsets, torch.Tensor):
         raise TypeError("offsets must be a torch tensor")
@@ -851,6 +872,12 @@ def qgemm_expert_plan(ids, experts, out=None, workspace=None):
     offsets[-1] on), places[t, j] the row of a token's choice (-1: none).
     `out` may be a tuple of those three to write into; workspace: uint8, at least
     qgemm_expert_plan_workspace_bytes(tokens * top, experts), allocated if None."""
+    status = None
+    if _native and out is not None and workspace is not None:
+        status = _native.expert_plan(ids, experts, out, workspace)
+    if status is not None:
+        _check(status, "qgemm_expert_plan")
+        return out
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch tensor")
     device, experts = ids.get_device(), int(experts)
@@ -891,6 +918,12 @@ def qgemm_expert_combine(y, places, gates, out=None):
     order of j, rounded once: y [rows, N] float16 or bfloat16, places int32
     [tokens, top] (outside 0 .. rows - 1: left out), gates float32 [tokens, top].
     Returns out, [tokens, N] of y's type."""
+    status = None
+    if _native and out is not None:
+        status = _native.expert_combine(y, places, gates, out)
+    if status is not None:
+        _check(status, "qgemm_expert_combine")
+        return out
     if not isinstance(y, torch.Tensor):
         raise TypeError("y must be a torch tensor")
     device = y.get_device()

@@ -1,6 +1,7 @@
-// The short way into the key-value cache calls: argument checks and the call
-// itself in native code, for arguments as a serving loop passes them (tensors
-// of one device, outputs and workspace given).  Such a call is made for every
+// The short way into the calls of a serving loop, those of the key-value cache and
+// of int8 and expert layers: argument checks and the call itself in native code, for
+// arguments as such a loop passes them (tensors of one device, outputs and workspace
+// given).  Such a call is made for every
 // layer of every step, and its checks in Python take longer than the kernels
 // run.  Each function returns the call's status, or None for anything that it
 // does not take; the Python function of the same name then checks the
@@ -9,12 +10,14 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <utility>
 
 #include "qgemm.h"
 
 namespace {
 
 PyObject* stream_of = nullptr;   // torch's device number -> current stream
+PyObject* device_of = nullptr;   // torch's current device number
 
 // Conditions that the Python side spells out: thrown over, never shown.
 struct NotPlain {};
@@ -208,10 +211,175 @@ PyObject* paged_attention(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
   });
 }
 
+// ---- int8 x int8 products, dense and by expert ---------------------------------
+
+// The tensor's device is the current one: the calls launch there.
+void need_current(const at::Tensor& t) {
+  PyObject* now = PyObject_CallNoArgs(device_of);
+  need(now != nullptr);
+  const long device = PyLong_AsLong(now);
+  Py_DECREF(now);
+  need(!PyErr_Occurred() && device == t.get_device());
+}
+
+int flag(PyObject* o) {
+  need(PyBool_Check(o));
+  return o == Py_True;
+}
+
+// (x, out)
+PyObject* quantize_int8(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+  return guarded([&]() -> PyObject* {
+    need(nargs == 2 && PyTuple_CheckExact(arg[1]) && PyTuple_GET_SIZE(arg[1]) == 2);
+    const at::Tensor& x = view(arg[0], 2);
+    const auto s = x.scalar_type();
+    need(s == at::kHalf || s == at::kBFloat16 || s == at::kFloat);
+    const int type = s == at::kHalf ? QGEMM_F16 : s == at::kBFloat16 ? QGEMM_BF16 : QGEMM_F32;
+    const int64_t rows = x.size(0), K = x.size(1);
+    PyObject* const* out = &PyTuple_GET_ITEM(arg[1], 0);
+    int8_t* codes = static_cast<int8_t*>(dense(out[0], at::kChar, 2, rows, x));
+    need(THPVariable_Unpack(out[0]).size(1) == K);
+    float* scale = static_cast<float*>(dense(out[1], at::kFloat, 1, rows, x));
+    need_current(x);
+    const void* p = x.data_ptr();
+    const int64_t step = stride(x, 0);
+    void* st = stream(x);
+    return status_of([&] { return qgemm_quantize_int8(type, p, codes, scale, rows, K, step, st); });
+  });
+}
+
+// Operands of both products.
+struct W8a8Operands {
+  const int8_t* a;
+  const float* a_scale;
+  const void* packed;
+  int64_t rows, K;
+
+  W8a8Operands(const at::Tensor& first, PyObject* a_, PyObject* scale, PyObject* w, int64_t experts,
+               int64_t N, int gated) {
+    a = static_cast<const int8_t*>(dense(a_, at::kChar, 2, -1, first));
+    rows = first.size(0), K = first.size(1);
+    a_scale = static_cast<const float*>(dense(scale, at::kFloat, 1, rows, first));
+    packed = dense(w, at::kByte, 1, -1, first);
+    const int64_t bytes = qgemm_prepack_w8a8_bytes(experts, K, N, gated);
+    need(bytes >= 0 && THPVariable_Unpack(w).size(0) >= bytes);
+  }
+};
+
+// The output given: its type and address.
+std::pair<int, void*> product_out(PyObject* o, int64_t M, int64_t cols, const at::Tensor& first) {
+  const at::Tensor& t = tensor(o, 2);
+  const int type = half_type(t);
+  void* p = dense(o, t.scalar_type(), 2, M, first);
+  need(t.size(1) == cols);
+  return {type, p};
+}
+
+// (a, a_scale, w_packed, w_scale, N, gated, out)
+PyObject* w8a8(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+  return guarded([&]() -> PyObject* {
+    need(nargs == 7);
+    const at::Tensor& a = tensor(arg[0], 2);
+    const int64_t N = integer(arg[4]);
+    const int gated = flag(arg[5]);
+    const W8a8Operands x(a, arg[0], arg[1], arg[2], 1, N, gated);
+    const float* w_scale = static_cast<const float*>(dense(arg[3], at::kFloat, 1, N, a));
+    const auto out = product_out(arg[6], x.rows, gated ? N / 2 : N, a);
+    need_current(a);
+    void* st = stream(a);
+    return status_of([&] {
+      return qgemm_w8a8(out.first, x.a, x.a_scale, x.packed, w_scale, out.second, x.rows, N, x.K, gated,
+                        st);
+    });
+  });
+}
+
+// (a, a_scale, w_packed, w_scale, offsets, N, rows, gated, out)
+PyObject* w8a8_experts(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+  return guarded([&]() -> PyObject* {
+    need(nargs == 9);
+    const at::Tensor& a = tensor(arg[0], 2);
+    const int64_t N = integer(arg[5]);
+    const int gated = flag(arg[7]);
+    const int32_t* offsets = static_cast<const int32_t*>(dense(arg[4], at::kInt, 1, -1, a));
+    const int64_t experts = THPVariable_Unpack(arg[4]).size(0) - 1;
+    need(experts >= 1);
+    const W8a8Operands x(a, arg[0], arg[1], arg[2], experts, N, gated);
+    const float* w_scale = static_cast<const float*>(dense(arg[3], at::kFloat, 2, experts, a));
+    need(THPVariable_Unpack(arg[3]).size(1) == N);
+    int64_t M = x.rows;
+    const int32_t* rows = nullptr;
+    if (arg[6] != Py_None) {
+      rows = static_cast<const int32_t*>(dense(arg[6], at::kInt, 1, -1, a));
+      M = THPVariable_Unpack(arg[6]).size(0);
+    }
+    const auto out = product_out(arg[8], M, gated ? N / 2 : N, a);
+    need_current(a);
+    void* st = stream(a);
+    return status_of([&] {
+      return qgemm_w8a8_experts(out.first, x.a, x.a_scale, x.packed, w_scale, offsets, rows, out.second,
+                                x.rows, M, N, x.K, experts, gated, st);
+    });
+  });
+}
+
+// (ids, experts, out, workspace)
+PyObject* expert_plan(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+  return guarded([&]() -> PyObject* {
+    need(nargs == 4 && PyTuple_CheckExact(arg[2]) && PyTuple_GET_SIZE(arg[2]) == 3);
+    const at::Tensor& ids = tensor(arg[0], 2);
+    const auto s = ids.scalar_type();
+    need((s == at::kInt || s == at::kLong) && ids.is_contiguous());
+    const int64_t tokens = ids.size(0), top = ids.size(1), experts = integer(arg[1]);
+    const int64_t bytes = qgemm_expert_plan_workspace_bytes(tokens * top, experts);
+    need(bytes >= 0);
+    PyObject* const* out = &PyTuple_GET_ITEM(arg[2], 0);
+    int32_t* offsets = static_cast<int32_t*>(dense(out[0], at::kInt, 1, experts + 1, ids));
+    int32_t* rows = static_cast<int32_t*>(dense(out[1], at::kInt, 1, tokens * top, ids));
+    int32_t* places = static_cast<int32_t*>(dense(out[2], at::kInt, 2, tokens, ids));
+    need(THPVariable_Unpack(out[2]).size(1) == top);
+    void* workspace = dense(arg[3], at::kByte, 1, -1, ids);
+    need(THPVariable_Unpack(arg[3]).size(0) >= bytes);
+    need_current(ids);
+    const void* p = ids.data_ptr();
+    void* st = stream(ids);
+    return status_of([&] {
+      return qgemm_expert_plan(s == at::kInt ? 4 : 8, p, offsets, rows, places, workspace, tokens, top,
+                               experts, st);
+    });
+  });
+}
+
+// (y, places, gates, out)
+PyObject* expert_combine(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+  return guarded([&]() -> PyObject* {
+    need(nargs == 4);
+    const at::Tensor& y = tensor(arg[0], 2);
+    const int type = half_type(y);
+    need(y.is_contiguous());
+    const int32_t* places = static_cast<const int32_t*>(dense(arg[1], at::kInt, 2, -1, y));
+    const int64_t tokens = THPVariable_Unpack(arg[1]).size(0), top = THPVariable_Unpack(arg[1]).size(1);
+    const float* gates = static_cast<const float*>(dense(arg[2], at::kFloat, 2, tokens, y));
+    need(THPVariable_Unpack(arg[2]).size(1) == top);
+    void* out = dense(arg[3], y.scalar_type(), 2, tokens, y);
+    need(THPVariable_Unpack(arg[3]).size(1) == y.size(1));
+    need_current(y);
+    const void* p = y.data_ptr();
+    const int64_t rows = y.size(0), N = y.size(1);
+    void* st = stream(y);
+    return status_of([&] { return qgemm_expert_combine(type, p, places, gates, out, rows, tokens, top, N, st); });
+  });
+}
+
 PyMethodDef methods[] = {
     {"kv_plan", (PyCFunction)(void (*)())kv_plan, METH_FASTCALL, nullptr},
     {"kv_append", (PyCFunction)(void (*)())kv_append, METH_FASTCALL, nullptr},
     {"paged_attention", (PyCFunction)(void (*)())paged_attention, METH_FASTCALL, nullptr},
+    {"quantize_int8", (PyCFunction)(void (*)())quantize_int8, METH_FASTCALL, nullptr},
+    {"w8a8", (PyCFunction)(void (*)())w8a8, METH_FASTCALL, nullptr},
+    {"w8a8_experts", (PyCFunction)(void (*)())w8a8_experts, METH_FASTCALL, nullptr},
+    {"expert_plan", (PyCFunction)(void (*)())expert_plan, METH_FASTCALL, nullptr},
+    {"expert_combine", (PyCFunction)(void (*)())expert_combine, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
@@ -224,7 +392,8 @@ PyMODINIT_FUNC PyInit__binding() {
   PyObject* torch_c = PyImport_ImportModule("torch._C");
   if (!torch_c) return nullptr;
   stream_of = PyObject_GetAttrString(torch_c, "_cuda_getCurrentRawStream");
+  device_of = PyObject_GetAttrString(torch_c, "_cuda_getDevice");
   Py_DECREF(torch_c);
-  if (!stream_of) return nullptr;
+  if (!stream_of || !device_of) return nullptr;
   return PyModule_Create(&module);
 }

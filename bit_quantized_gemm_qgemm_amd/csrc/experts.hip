@@ -18,9 +18,9 @@ namespace {
 // is the pairs' own.  The counts of the waves, and of the workgroups before, then
 // become places.
 //
-// Where several workgroups share the pairs, a launch ahead leaves each workgroup's counts in the workspace, expert by expert, where a wave
-// of the second sums 64 workgroups' at once.
-// A workgroup of THREADS takes ROUNDS pairs a thread, of up to EXPERTS experts.
+// Where several workgroups share the pairs, a launch ahead leaves their counts in the
+// workspace, and each workgroup of the second sums those it needs.
+
 template <int THREADS_, int ROUNDS_, int EXPERTS_>
 struct PlanShape {
   static constexpr int THREADS = THREADS_, ROUNDS = ROUNDS_, EXPERTS = EXPERTS_;
@@ -33,10 +33,9 @@ struct PlanState {
   int at[S::ROUNDS];   // place among the wave's pairs of that expert
 };
 
-// counts [wave][experts] in LDS; pair (wave * ROUNDS + r) * 64 + lane of the share
+// pair (wave * ROUNDS + r) * 64 + lane of the share
 template <class S>
-__device__ __forceinline__ void count_pairs(PlanState<S>& s, const ExpertPlan& p, int64_t first,
-                                            int* counts) {
+__device__ __forceinline__ void load_pairs(PlanState<S>& s, const ExpertPlan& p, int64_t first) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int r = 0; r < S::ROUNDS; ++r) {
@@ -46,6 +45,12 @@ __device__ __forceinline__ void count_pairs(PlanState<S>& s, const ExpertPlan& p
       id = p.wide ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
     s.e[r] = id >= 0 && id < p.experts ? (int)id : -1;
   }
+}
+
+// counts [wave][experts] in LDS
+template <class S>
+__device__ __forceinline__ void count_pairs(PlanState<S>& s, const ExpertPlan& p, int* counts) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int i = threadIdx.x; i < S::kWaves * p.experts; i += S::THREADS) counts[i] = 0;
   const int bits = 32 - __builtin_clz(p.experts);   // of 0 .. experts
   __syncthreads();
@@ -76,49 +81,42 @@ template <class S>
 __global__ __launch_bounds__(S::THREADS) void expert_count_kernel(const ExpertPlan p) {
   __shared__ int counts[S::kWaves * S::EXPERTS];
   PlanState<S> s;
-  count_pairs<S>(s, p, (int64_t)blockIdx.x * S::kPairs, counts);
+  load_pairs<S>(s, p, (int64_t)blockIdx.x * S::kPairs);
+  count_pairs<S>(s, p, counts);
   for (int e = threadIdx.x; e < p.experts; e += S::THREADS) {
     int n = 0;
 #pragma unroll
     for (int w = 0; w < S::kWaves; ++w) n += counts[w * p.experts + e];
-    p.counts[(int64_t)e * gridDim.x + blockIdx.x] = n;
+    p.counts[(int64_t)blockIdx.x * p.experts + e] = n;
   }
 }
 
 template <class S>
 __global__ __launch_bounds__(S::THREADS) void expert_place_kernel(const ExpertPlan p) {
   __shared__ int counts[S::kWaves * S::EXPERTS];
-  __shared__ int earlier[S::EXPERTS], all[S::EXPERTS];   // pairs of the workgroups before, and of all
+  constexpr int kParts = S::THREADS / S::EXPERTS;   // threads that sum the workgroups' counts of an expert
+  __shared__ int earlier[kParts][S::EXPERTS], all[kParts][S::EXPERTS];   // of the workgroups before, of all
   __shared__ int wave_sum[S::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t first = (int64_t)blockIdx.x * S::kPairs;
   const int groups = gridDim.x;
-  if (groups > 1) {
-    // experts wave, wave + kWaves, ...: the counts of all of them in flight at once
-    constexpr int kEach = S::EXPERTS / S::kWaves;
-    for (int b0 = 0; b0 < groups; b0 += 64) {
-      const int mine = (int)blockIdx.x - b0;   // workgroups of these 64 before this one
-      int n[kEach];
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        const int e = wave + j * S::kWaves;
-        n[j] = e < p.experts && b0 + lane < groups ? p.counts[(int64_t)e * groups + b0 + lane] : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        const int e = wave + j * S::kWaves;
-        const int upto = int_sums_of_wave(n[j]);
-        const int sum = __builtin_amdgcn_readlane(upto, 63);
-        const int before = mine <= 0 ? 0 : mine < 64 ? __builtin_amdgcn_readlane(upto, mine - 1) : sum;
-        if (lane == 0 && e < p.experts) {
-          earlier[e] = (b0 > 0 ? earlier[e] : 0) + before;
-          all[e] = (b0 > 0 ? all[e] : 0) + sum;
-        }
-      }
-    }
-  }
   PlanState<S> s;
-  count_pairs<S>(s, p, first, counts);
+  load_pairs<S>(s, p, first);
+  // Plain sums of a thread, eight loads in flight: sums of a wave over its lanes took
+  // half of the kernel's time (32768 tokens x 8 of 256 experts: 17.5 -> 13.4 us).
+  const int part = tid / S::EXPERTS, mine = tid % S::EXPERTS;
+  if (groups > 1 && mine < p.experts) {
+    int sum = 0, before = 0;   // of the workgroups from this one on, of those before it
+    const int32_t* left = p.counts + mine;
+    int b = part;
+#pragma unroll 8
+    for (; b < (int)blockIdx.x; b += kParts) before += left[(int64_t)b * p.experts];
+#pragma unroll 8
+    for (; b < groups; b += kParts) sum += left[(int64_t)b * p.experts];
+    earlier[part][mine] = before;
+    all[part][mine] = before + sum;
+  }
+  count_pairs<S>(s, p, counts);
 
   // sums over the experts, THREADS of them at a time
   int before = 0;   // pairs of the experts of the rounds before
@@ -128,10 +126,12 @@ __global__ __launch_bounds__(S::THREADS) void expert_place_kernel(const ExpertPl
 #pragma unroll
     for (int w = 0; w < S::kWaves; ++w) n[w] = e < p.experts ? counts[w * p.experts + e] : 0;
     if (groups > 1) {
-      if (e < p.experts) {
-        at = earlier[e];
-        total = all[e];
-      }
+      if (e < p.experts)
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          at += earlier[i][e];
+          total += all[i][e];
+        }
     } else {
 #pragma unroll
       for (int w = 0; w < S::kWaves; ++w) total += n[w];
@@ -258,13 +258,16 @@ hipError_t launch_plan(const ExpertPlan& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Pairs of a workgroup.  One does up to 4096 (512 tokens x 8 of 128 experts 7.3 us;
-// two of 2048 with their second launch 11.0, 600 tokens 11.0, 14.2 with shares of
-// 4096).  Shares of 2048 end sooner up to 2^18 pairs (16384 pairs 12.4 us, 15.6 with
-// 4096 and 23.5 with 8192; 262144 pairs of 256 experts 18.0, 17.5, 25.1), above that
-// the second launch's sums over all of them do not (2^22: 593, 176 and 73).
-constexpr int64_t kPlanAlone = 4096, kPlanMany = (int64_t)1 << 18;
-int64_t plan_share(int64_t pairs) { return pairs <= kPlanAlone ? kPlanAlone : pairs <= kPlanMany ? 2048 : 8192; }
+// Pairs of a workgroup.  One does up to 4096 (512 tokens x 8 of 128 experts 7.2 us; two
+// of 2048 with their second launch 8.3; 600 tokens: 8.4, with shares of 4096 11.7).
+// Above it shares of 2048 end soonest (2^14 pairs of 256 experts 9.4 us, 12.9 with
+// shares of 4096 and 20.2 with 8192; 2^18 13.5, 16.1, 23.4; 2^19 of 128 15.4, 17.1,
+// 22.7) until the sums over all the workgroups, in each of them, weigh more (2^20: 29.6,
+// 21.4, 25.7; 2^22 of 16: 187, 75, 50).
+constexpr int64_t kPlanAlone = 4096, kPlanMany = (int64_t)1 << 19, kPlanMost = (int64_t)1 << 20;
+int64_t plan_share(int64_t pairs) {
+  return pairs <= kPlanAlone ? 4096 : pairs <= kPlanMany ? 2048 : pairs <= kPlanMost ? 4096 : 8192;
+}
 
 template <int EXPERTS>
 hipError_t launch_plan_of(const ExpertPlan& p, hipStream_t stream) {
@@ -278,8 +281,11 @@ hipError_t launch_plan_of(const ExpertPlan& p, hipStream_t stream) {
 }  // namespace
 
 int64_t expert_plan_workspace(int64_t pairs, int64_t experts) {
-  const int64_t groups = cdiv(pairs, plan_share(pairs));
-  return groups > 1 ? groups * experts * (int64_t)sizeof(int) : 0;
+  if (pairs <= kPlanAlone) return 0;
+  // no less than fewer pairs need, so that one sized for the most serves them all
+  int64_t groups = cdiv(pairs, plan_share(pairs)), fewer = cdiv(pairs < kPlanMany ? pairs : kPlanMany, 2048);
+  if (groups < fewer) groups = fewer;
+  return groups * experts * (int64_t)sizeof(int);
 }
 
 // Few pairs take four waves (32 tokens x 8 of 128 experts: 5.1 -> 2.4 us, with one

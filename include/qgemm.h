@@ -528,8 +528,9 @@ int qgemm_w8a8_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int gated,
  *   rows [tokens * top]    token of each sorted row; -1 from offsets[experts] on
  *   places [tokens, top]   sorted row of each pair; -1 where it has none
  * all int32.  tokens * top is at most 2^22.  workspace:
- * qgemm_expert_plan_workspace_bytes(tokens * top, experts) bytes, 16-byte aligned, of any contents;
- * calls that share one must not overlap.  May be NULL where that size is 0.
+ * qgemm_expert_plan_workspace_bytes(tokens * top, experts) bytes or more, 16-byte aligned,
+ * of any contents (the size for the most pairs serves fewer too); calls that share one must
+ * not overlap.  May be NULL where that size is 0.
  */
 int64_t qgemm_expert_plan_workspace_bytes(int64_t pairs, int64_t experts);
 int qgemm_expert_plan(int id_bytes, const void* ids, int32_t* offsets, int32_t* rows,

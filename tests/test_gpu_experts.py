@@ -43,6 +43,7 @@ def plan_case(ids, experts, dtype=torch.int64):
 @pytest.mark.parametrize("tokens,top,experts", [
     (1, 1, 1), (1, 8, 64), (7, 3, 5), (32, 8, 128), (64, 1, 2), (65, 2, 63), (100, 6, 64), (513, 4, 65),
     (1000, 8, 256), (1024, 8, 257), (1025, 8, 60), (2049, 8, 1024), (5000, 5, 1000), (9000, 8, 16), (600, 8, 300), (33000, 8, 20), (40000, 7, 1024),
+    (70000, 8, 40), (70000, 9, 257), (2 ** 20 // 8 + 1, 8, 256), (150000, 7, 1000),
 ])
 def test_plan_matches_the_oracle(tokens, top, experts, dtype):
     rng = np.random.default_rng(tokens + experts)
@@ -176,3 +177,53 @@ def test_a_whole_layer(tokens, dtype):
                 y = x[t].double().cpu() @ d1[e]
                 ref[t] += float(gates[t, j]) * ((torch.nn.functional.silu(y[:F]) * y[F:]) @ d2[e])
     assert float((got - ref).norm()) <= 2.0 ** -3 * float(ref.norm())
+
+
+def layer_inputs(tokens, seed):
+    K, F, E, top, dtype = 256, 96, 10, 3, torch.bfloat16
+    g = torch.Generator("cuda").manual_seed(seed)
+    weights = []
+    for k, n, gated in ((K, 2 * F, True), (F, K, False)):
+        w = torch.randint(-127, 128, (E, k, n), generator=g, device="cuda", dtype=torch.int8)
+        s = torch.rand((E, n), generator=g, device="cuda") / (74 * k ** 0.5)
+        weights.append((qg.qgemm_prepack_w8a8(w, gated=gated), s))
+    x = torch.randn((tokens, K), generator=g, device="cuda").to(dtype)
+    ids = torch.randint(0, E + 2, (tokens, top), generator=g, device="cuda")
+    return x, ids, torch.rand((tokens, top), generator=g, device="cuda"), weights, F, E
+
+
+@pytest.mark.parametrize("tokens", [2, 2000])
+def test_a_captured_layer_follows_its_inputs(tokens):
+    """One graph for any routing: the sizes of the experts are read on the device."""
+    print("case captured layer", tokens, flush=True)
+    x, ids, gates, weights, F, E = layer_inputs(tokens, 1)
+    layer(x, ids, gates, weights, F, E)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer(x, ids, gates, weights, F, E)
+    for i in range(4):
+        ids.copy_(torch.randint(-1, E // (i + 1) + 1, ids.shape, device="cuda"))
+        x.copy_(torch.randn(x.shape, device="cuda"))
+        want = layer(x, ids, gates, weights, F, E)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        out.zero_()
+
+
+def test_layers_on_two_streams():
+    """Calls on different streams with storage of their own do not disturb each other."""
+    print("case layers on two streams", flush=True)
+    inputs = [layer_inputs(tokens, tokens) for tokens in (1500, 37)]
+    want = [layer(*i) for i in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in inputs]
+    got = [[], []]
+    for _ in range(5):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(layer(*inputs[i]))
+    torch.cuda.synchronize()
+    for outs, ref in zip(got, want):
+        assert all(torch.equal(o, ref) for o in outs)

@@ -123,6 +123,9 @@ def test_sizes(lib):
     w = lib.qgemm_expert_plan_workspace_bytes
     assert w(0, 1) == 0 and w(4096, 1024) == 0 and w(4097, 7) == 3 * 7 * 4
     assert w(1 << 22, 1024) == (1 << 22) // 8192 * 1024 * 4
+    # a workspace for the most pairs serves fewer
+    sizes = [w(n, 7) for n in range(0, (1 << 22) + 1, 1024)] + [w(1 << 22, 7)]
+    assert sizes == sorted(sizes)
     for bad in ((-1, 4), ((1 << 22) + 1, 4), (5, 0), (5, 1025)):
         assert w(*bad) == ERR_SHAPE
     with pytest.raises(qg.QgemmError):

@@ -161,7 +161,9 @@ __device__ __forceinline__ uint16_t rounded(float v, bool bf16) {
 // A workgroup owns 16 rows and G column groups of 16; its NW waves share the K
 // tiles.  Weight tiles go from memory straight into registers, two of a wave in
 // flight, and meet the rows' codes in 16 x 16 x 64 matrix instructions; the waves'
-// sums meet in LDS.
+// sums meet in LDS.  The weight's bytes bound it: 64 experts of 4096 x 2048, of which
+// 16 tokens x 8 reach 53, take 67 us (446 MB: 6.7 TB/s, a plain read 7.07), one row by
+// 4096 x 11008 9.1 to 9.6 (45 MB, of which 3 us are the launch and the way in and out).
 template <int G>
 struct SlabTile {
   uintx4 x[2], w[G][2];
@@ -314,6 +316,14 @@ hipError_t launch_slab(const W8a8& p, hipStream_t stream) {
 // Per slice u, between the matrix instructions: the LDS reads of the next slice's
 // codes, the weight fragments of slice u of step s + WB - 1, and a share of the
 // copies of step s + 3; after slice 2 the wait for the copies of step s + 1.
+//
+// What bounds the largest tiles is power: 8192 x 8192 x 8192 takes 422 us (2.6 POP/s)
+// with the matrix pipe busy 72 % of it at 1.65 GHz, where these instructions alone, on
+// codes of all sizes, run at 3.3 POP/s and 1.54 GHz (on zeros at 4.7).  What bounds
+// the middle ones is the way from the L2 to the CUs, 17 TB/s in all, and below some
+// ten steps the way in and out: 300 rows by 4096 x 11008, gated, 19 us with the weight
+// in the Infinity Cache, 28.7 from memory.  The weight does not pass through LDS:
+// each fragment is read by one wave, or by two, that its CU's cache partly serves.
 template <int FM_, int FN_, int WR_, int WC_, int KS_, int WB_, int NS_ = 4>
 struct Tile {
   static constexpr int FM = FM_, FN = FN_, WR = WR_, WC = WC_, KS = KS_, WB = WB_, NS = NS_;

@@ -355,6 +355,8 @@ int check_apart(std::initializer_list<Bytes> outputs, std::initializer_list<Byte
 
 // The sum of K products of two codes stays within 32 bits: 2^14 K < 2^31.
 constexpr int64_t kMaxInt8K = 131056;
+// Rows of a product: a launch has less than 2^32 threads.
+constexpr int64_t kMaxInt8Rows = (int64_t)1 << 28;
 
 // One packed weight stays below 2^31 bytes (32-bit offsets within it), all of
 // them below 2^40.
@@ -362,7 +364,7 @@ int check_w8a8_weight(int64_t experts, int64_t K, int64_t N, int gated) {
   if (!below(experts, 1, qgemm::kMaxExperts + 1) || !below(K, 0, kMaxInt8K + 1) || K % 16 != 0 ||
       !below(N, 0, kMaxIndex) || (gated != 0 && gated != 1) || (gated && N % 2 != 0))
     return QGEMM_ERR_SHAPE;
-  if ((N + 32) * qgemm::cdiv(K, 128) * 128 >= kMaxIndex) return QGEMM_ERR_SHAPE;
+  if ((N + 32) * qgemm::cdiv(K > 0 ? K : 1, 128) * 128 >= kMaxIndex) return QGEMM_ERR_SHAPE;
   return QGEMM_OK;
 }
 
@@ -376,7 +378,7 @@ int w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
   int st = check_w8a8_weight(weights, K, N, gated);
   if (st != QGEMM_OK) return st;
   const int64_t out_n = gated ? N / 2 : N;
-  if (!below(M, 0, kMaxIndex) || !below(a_rows, 0, kMaxIndex) || a_rows * K >= kMaxIndex ||
+  if (!below(M, 0, kMaxInt8Rows) || !below(a_rows, 0, kMaxIndex) || a_rows * K >= kMaxIndex ||
       M * N >= kMaxIndex || (!rows && M > 0 && a_rows != M))
     return QGEMM_ERR_SHAPE;
   const bool some = M > 0 && N > 0;
@@ -865,7 +867,7 @@ int qgemm_w8a8_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int gated,
                     int64_t* cols, int64_t* k_split) {
   const int st = check_w8a8_weight(experts == 0 ? 1 : experts, K, N, gated);
   if (st != QGEMM_OK) return st;
-  if (!below(M, 0, kMaxIndex) || M * N >= kMaxIndex) return QGEMM_ERR_SHAPE;
+  if (!below(M, 0, kMaxInt8Rows) || M * N >= kMaxIndex) return QGEMM_ERR_SHAPE;
   if (!rows || !cols || !k_split) return QGEMM_ERR_NULL;
   static const int32_t some = 0;
   qgemm::W8a8 p{};

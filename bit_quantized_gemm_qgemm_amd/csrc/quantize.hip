@@ -276,6 +276,13 @@ __device__ __forceinline__ float int8_scale(uint32_t top) {
                            : __builtin_bit_cast(float, 0x7fc00000u);
 }
 
+// Workgroups lie in two dimensions: one holds less than 2^32 threads.
+constexpr int64_t kAcross = (int64_t)1 << 20;
+inline dim3 grid_of(int64_t groups) {
+  return dim3((unsigned)(groups < kAcross ? groups : kAcross), (unsigned)cdiv(groups, kAcross));
+}
+__device__ __forceinline__ int64_t group_of_rows() { return blockIdx.y * kAcross + blockIdx.x; }
+
 // WAVES waves share a row and keep it in registers, 8 ROUNDS elements a lane;
 // workgroups of 4 waves, or of 16.  Memory bounds it: the row is read once, past the
 // caches (16384 rows of 8192 in bf16: 63 us, 6.4 TB/s read and written; of 4096 and
@@ -287,8 +294,8 @@ __global__ __launch_bounds__(WAVES > 4 ? 1024 : 256) void quantize_int8_kernel(
   constexpr int kPerGroup = WAVES == 1 ? 4 : 1;   // rows of a workgroup
   __shared__ uint32_t part[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = kPerGroup * (int64_t)blockIdx.x + (WAVES == 1 ? wave : 0);
-  if (row >= rows) return;   // a wave of its own
+  const int64_t row = kPerGroup * group_of_rows() + (WAVES == 1 ? wave : 0);
+  if (row >= rows) return;   // a wave of its own, or the whole workgroup
   const int first = 8 * (WAVES == 1 ? lane : (int)threadIdx.x);
   Eight<DT> v[ROUNDS];
 #pragma unroll
@@ -331,9 +338,11 @@ template <int DT>
 __global__ __launch_bounds__(1024) void quantize_int8_long_kernel(const void* __restrict__ x,
                                                                   int64_t row_stride,
                                                                   int8_t* __restrict__ codes,
-                                                                  float* __restrict__ scale, int K) {
+                                                                  float* __restrict__ scale,
+                                                                  int64_t rows, int K) {
   __shared__ uint32_t part[16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = group_of_rows();
+  if (row >= rows) return;   // the whole workgroup
   Largest<DT> m;
   Eight<DT> v;
   for (int k = 8 * threadIdx.x; k < K; k += 8192) {
@@ -361,8 +370,8 @@ template <int DT, int WAVES, int ROUNDS>
 void quantize_rows(const void* x, int64_t row_stride, int8_t* codes, float* scale, int64_t rows, int K,
                    hipStream_t stream) {
   hipLaunchKernelGGL((quantize_int8_kernel<DT, WAVES, ROUNDS>),
-                     dim3((unsigned)cdiv(rows, WAVES == 1 ? 4 : 1)), dim3(WAVES > 4 ? 1024 : 256), 0,
-                     stream, x, row_stride, codes, scale, rows, K);
+                     grid_of(cdiv(rows, WAVES == 1 ? 4 : 1)), dim3(WAVES > 4 ? 1024 : 256), 0, stream,
+                     x, row_stride, codes, scale, rows, K);
 }
 
 // Shapes by the row's length, us for bf16 rows of 50 M elements together and the next
@@ -390,8 +399,8 @@ hipError_t quantize_int8(const void* x, int64_t row_stride, int8_t* codes, float
   else if (K <= 65536)
     quantize_rows<DT, 16, 8>(x, row_stride, codes, scale, rows, K, stream);
   else
-    hipLaunchKernelGGL((quantize_int8_long_kernel<DT>), dim3((unsigned)rows), dim3(1024), 0, stream, x,
-                       row_stride, codes, scale, K);
+    hipLaunchKernelGGL((quantize_int8_long_kernel<DT>), grid_of(rows), dim3(1024), 0, stream, x,
+                       row_stride, codes, scale, rows, K);
   return hipGetLastError();
 }
 

@@ -81,11 +81,12 @@ __device__ __forceinline__ int2 rows_of(const Args& g, int e) {
 
 // The workgroups' items lie in one row: expert after expert, of each groups of
 // GROUP row blocks, of a group its column blocks in turn, and of a column block the
-// row blocks.  Workgroups are handed
-// to the 8 XCDs round-robin; each XCD takes an eighth of the row, so that the
-// row blocks that share a weight tile meet in one L2.  The experts' places
-// in the row follow from their row counts: a wave counts the blocks of all
-// experts, each lane those of `per` neighbours.
+// row blocks.  Workgroups are handed to the 8 XCDs round-robin; each XCD takes an
+// eighth of the row, so that the row blocks that share a weight tile meet in one L2.
+// The experts' places in the row follow from their row counts: a wave counts the
+// blocks of all experts, each lane those of `per` neighbours.  Offsets that do not
+// fall leave at most as many blocks as the launch has; of any others there are no
+// items.
 template <int BM, int GROUP>
 __device__ __forceinline__ Item item_of(const Args& g) {
   Item it{0, 0, g.M, 0, true};
@@ -96,15 +97,17 @@ __device__ __forceinline__ Item item_of(const Args& g) {
   int mine = 0, upto = 0;
   auto blocks_of = [](int2 r) { return (r.y - r.x + BM - 1) / BM; };
   if (g.offsets) {
+    bool falls = false;
     for (int j = 0; j < per; ++j) {
       const int e = lane * per + j;
       if (e < g.experts) {
         r = rows_of(g, e);
         mine += blocks_of(r);
+        falls |= g.offsets[e + 1] < g.offsets[e];
       }
     }
     upto = int_sums_of_wave(mine);
-    total = __builtin_amdgcn_readlane(upto, 63);
+    total = __ballot(falls) == 0 ? __builtin_amdgcn_readlane(upto, 63) : 0;
   }
   const int items = total * g.col_blocks, share = (items + 7) / 8;
   const int slot = blockIdx.x >> 3, i = (int)(blockIdx.x & 7) * share + slot;
@@ -324,9 +327,10 @@ hipError_t launch_slab(const W8a8& p, hipStream_t stream) {
 // ten steps the way in and out: 300 rows by 4096 x 11008, gated, 19 us with the weight
 // in the Infinity Cache, 28.7 from memory.  The weight does not pass through LDS:
 // each fragment is read by one wave, or by two, that its CU's cache partly serves.
-template <int FM_, int FN_, int WR_, int WC_, int KS_, int WB_, int NS_ = 4>
+template <int FM_, int FN_, int WR_, int WC_, int KS_, int WB_>
 struct Tile {
-  static constexpr int FM = FM_, FN = FN_, WR = WR_, WC = WC_, KS = KS_, WB = WB_, NS = NS_;
+  static constexpr int FM = FM_, FN = FN_, WR = WR_, WC = WC_, KS = KS_, WB = WB_;
+  static constexpr int NS = 4;   // stages of the ring
   static constexpr int kWaves = WR * WC * KS, kThreads = 64 * kWaves;
   static constexpr int kRows = 32 * FM * WR, kCols = 32 * FN * WC;
   static constexpr int kTileBytes = kRows * 128;          // the rows' codes of one K tile
@@ -482,7 +486,7 @@ __device__ __forceinline__ uint32_t rounded_pair(float lo, float hi) {
 }
 
 template <class T>
-__global__ __launch_bounds__(T::kThreads, T::kThreads / 256 > 1 ? 1 : T::FM * T::FN >= 10 || T::kLds > 81920 ? 1 : 2) void w8a8_tile_kernel(const Args g) {
+__global__ __launch_bounds__(T::kThreads, T::kThreads > 256 ? 1 : 2) void w8a8_tile_kernel(const Args g) {
   constexpr int FM = T::FM, FN = T::FN, WR = T::WR, WC = T::WC, KS = T::KS, WB = T::WB;
   // One array: with more than one the compiler tells them apart, takes the copies
   // into LDS for writes to any of them and waits for all memory before each read.

@@ -451,7 +451,8 @@ int qgemm_paged_attention(int dtype, int cache_dtype, const void* q, const void*
  *
  * Differing from the conventions above: fp32 and int32 arrays need 4-byte and
  * int64 arrays 8-byte alignment only, and an output that shares memory with an
- * input or another output is refused (QGEMM_ERR_OVERLAP).  K is a multiple of
+ * input (from its first element to its last) or another output is refused
+ * (QGEMM_ERR_OVERLAP).  K is a multiple of
  * 16 and at most 131056, so that a sum of K products of two codes fits 32 bits;
  * experts is 1 .. 1024.
  */
@@ -473,7 +474,7 @@ int qgemm_quantize_int8(int dtype, const void* x, int8_t* codes, float* scale, i
  * columns are two halves, gate and up (N even).  w_packed holds
  * qgemm_prepack_w8a8_bytes(...) bytes, all of which are written; one expert's
  * share, of N rounded up to a multiple of 16 (each half, if gated) and K to one
- * of 128, is below 2^31 bytes.
+ * of 128 (K = 0 too), is below 2^31 bytes, by 32 columns.
  */
 int64_t qgemm_prepack_w8a8_bytes(int64_t experts, int64_t K, int64_t N, int gated);
 int qgemm_prepack_w8a8(const int8_t* w, void* w_packed, int64_t experts, int64_t K, int64_t N,
@@ -487,8 +488,8 @@ int qgemm_prepack_w8a8(const int8_t* w, void* w_packed, int64_t experts, int64_t
  * a: int8 [M, K], any codes; a_scale fp32 [M]; w_packed from qgemm_prepack_w8a8
  * with the same K, N and gated; w_scale fp32 [N]; out: dtype (QGEMM_F16 or
  * QGEMM_BF16).  The sum is exact; it is rounded to fp32, multiplied by a_scale
- * and then by w_scale in fp32, and the result is rounded once.  M * K and M * N
- * are below 2^31.
+ * and then by w_scale in fp32, and the result is rounded once.  M is below 2^28,
+ * M * K and M * N below 2^31.
  */
 int qgemm_w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
                const float* w_scale, void* out, int64_t M, int64_t N, int64_t K, int gated,
@@ -499,10 +500,11 @@ int qgemm_w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_p
  * of the M rows of out, offsets[e] <= m < offsets[e + 1], takes W[e] and
  * w_scale[e] ([experts, N]).  offsets int32 [experts + 1] on the device must not
  * fall; they are held to 0 .. M, rows before the first and from the last on are
- * left as they were, and an expert may have no rows.  (Where offsets fall, rows
- * of out are unspecified.)  rows NULL: row m reads row m of a and a_scale, and
+ * left as they were, and an expert may have no rows.  (Where offsets fall, all of
+ * out is left as it was.)  rows NULL: row m reads row m of a and a_scale, and
  * a_rows is M.  Otherwise rows int32 [M] names the row, 0 .. a_rows - 1, that
- * each reads; one outside gives a row of zeros.  a_rows * K is below 2^31.
+ * each reads; one outside stands for codes and a scale of 0.  a_rows * K is below
+ * 2^31.
  */
 int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
                        const float* w_scale, const int32_t* offsets, const int32_t* rows, void* out,

@@ -80,6 +80,25 @@ def test_strided_rows_and_given_outputs(dtype):
     assert codes.shape == (0, 64) and scale.shape == (0,)
 
 
+def test_more_rows_than_one_dimension_holds():
+    """2^26 rows of 16 and 2^24 of 2064: workgroups of 256 threads, 2^32 and more of them together."""
+    print("case quantize int8 many rows", flush=True)
+    pattern = torch.randn((1025, 16), device="cuda").bfloat16()
+    want = qg.qgemm_quantize_int8(pattern)
+    times = 2 ** 26 // 1025 + 2
+    codes, scale = qg.qgemm_quantize_int8(pattern.repeat(times, 1))
+    assert torch.equal(codes.view(times, -1), want[0].view(1, -1).expand(times, -1))
+    assert torch.equal(scale.view(times, -1), want[1].view(1, -1).expand(times, -1))
+    del codes, scale
+    row, rows = torch.randn((1, 2064), device="cuda").bfloat16(), 2 ** 24 + 3
+    want = qg.qgemm_quantize_int8(row)
+    out = (torch.empty((rows, 2064), dtype=torch.int8, device="cuda"), torch.zeros(rows, device="cuda"))
+    qg.qgemm_quantize_int8(row.expand(rows, 2064), out=out)
+    assert (out[1] == want[1]).all()
+    for r in (0, 1, 2 ** 20 - 1, 2 ** 20, 2 ** 23 + 5, 2 ** 24 - 1, 2 ** 24, rows - 1):
+        assert torch.equal(out[0][r], want[0][0])
+
+
 def test_on_another_stream_and_in_a_graph():
     print("case quantize int8 graph", flush=True)
     x = torch.randn((31, 4096), device="cuda").to(torch.bfloat16)

@@ -238,12 +238,24 @@ def test_offsets_outside_the_rows():
     ref, bound, touched = oracle.gemm_w8a8_experts(a, sa, w, sw, offsets, None, np.full((20, 24), 7.0))
     assert touched.all()
     close(out, ref, bound, torch.bfloat16)
-    # falling offsets: the rows of out are unspecified, nothing else is
+    # falling offsets: nothing is written
     guard = torch.full((40, 24), 7.0, dtype=torch.bfloat16, device="cuda")
     qg.qgemm_w8a8_experts(dev(a), dev(sa), qg.qgemm_prepack_w8a8(dev(w)), dev(sw),
                           dev(np.array([15, 3, 20, 0], np.int32)), 24, out=guard[10:30])
     torch.cuda.synchronize()
-    assert (guard[:10] == 7).all() and (guard[30:] == 7).all()
+    assert (guard == 7).all()
+
+
+def test_falling_offsets_of_many_experts():
+    """Row counts that add up to more than 2^31 items."""
+    print("case w8a8 falling offsets", flush=True)
+    experts, M, K, N = 1024, 60000, 16, 32768
+    zeros = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")
+    offsets = torch.arange(experts + 1, dtype=torch.int32, device="cuda") % 2 * M
+    out = torch.full((M, N), 7.0, dtype=torch.float16, device="cuda")
+    packed = zeros(qg.qgemm_prepack_w8a8_bytes(experts, K, N), dtype=torch.uint8)
+    qg.qgemm_w8a8_experts(zeros(M, K, dtype=torch.int8), zeros(M), packed, zeros(experts, N), offsets, N, out=out)
+    assert (out == 7).all()
 
 
 def test_expert_weights_past_four_gigabytes():

@@ -112,6 +112,14 @@ def test_other_architectures_are_refused(lib, monkeypatch):
         assert call(getattr(lib, name), base) == ERR_ARCH
 
 
+def test_most_rows(lib, monkeypatch):
+    """A launch holds a product's rows in one dimension of its grid."""
+    monkeypatch.setenv("QGEMM_ARCH_OVERRIDE", "gfx942")    # what passes the checks ends there
+    for M, status in (((1 << 28) - 1, ERR_ARCH), (1 << 28, ERR_SHAPE)):
+        assert call(lib.qgemm_w8a8, DENSE, M=M, K=0, N=2) == status
+        assert call(lib.qgemm_w8a8_experts, EXPERTS, M=M, N=2) == status
+
+
 def test_sizes(lib):
     n = lib.qgemm_prepack_w8a8_bytes
     assert n(1, 4096, 11008, 0) == 4096 * 11008
@@ -120,6 +128,7 @@ def test_sizes(lib):
     assert n(7, 0, 5, 0) == 0 and n(7, 16, 0, 0) == 0
     for bad in ((0, 16, 16, 0), (1, 8, 16, 0), (1, 16, -1, 0), (1, 16, 15, 1), (1, 16, 16, 2), (1, 131072, 16, 0)):
         assert n(*bad) == ERR_SHAPE
+    assert n(1, 0, (1 << 24) - 33, 0) == 0 and n(1, 0, (1 << 24) - 32, 0) == ERR_SHAPE
     w = lib.qgemm_expert_plan_workspace_bytes
     assert w(0, 1) == 0 and w(4096, 1024) == 0 and w(4097, 7) == 3 * 7 * 4
     assert w(1 << 22, 1024) == (1 << 22) // 8192 * 1024 * 4

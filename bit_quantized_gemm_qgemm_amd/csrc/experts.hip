@@ -18,17 +18,19 @@ namespace {
 // is the pairs' own.  The counts of the waves, and of the workgroups before, then
 // become places.
 //
-// Where several workgroups share the pairs, a launch ahead leaves their counts in the
-// workspace, and each workgroup of the second sums those it needs.
+// Where several workgroups share the pairs, a first launch leaves each workgroup's counts
+// in the workspace and each pair's place among its workgroup's pairs of its expert in
+// `places`; in the second each workgroup sums the counts that it needs.
 //
 // The bytes are few (32768 tokens x 8: 4.2 MB, below a microsecond); what it takes are
 // trips to memory and barriers one after the other: 2.4 us for 32 tokens x 8 of 128
-// experts, and for 32768 x 8 of 256 experts 4.1 of counts and 9.7 of places.
-
+// experts, 5.5 for 512 x 8, and for 32768 x 8 of 256 3.8 of counts and 6.2 of places.
 template <int THREADS_, int ROUNDS_, int EXPERTS_>
 struct PlanShape {
   static constexpr int THREADS = THREADS_, ROUNDS = ROUNDS_, EXPERTS = EXPERTS_;
-  static constexpr int kWaves = THREADS / 64, kPairs = THREADS * ROUNDS;
+  static constexpr int kWaves = THREADS / 64;
+  static constexpr int64_t kPairs = THREADS * ROUNDS;
+  static_assert(THREADS >= EXPERTS, "a thread for each expert");
 };
 
 template <class S>
@@ -37,6 +39,12 @@ struct PlanState {
   int at[S::ROUNDS];   // place among the wave's pairs of that expert
 };
 
+// Expert of pair i, or -1.
+__device__ __forceinline__ int expert_of(const ExpertPlan& p, int64_t i) {
+  const int64_t id = p.wide ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
+  return id >= 0 && id < p.experts ? (int)id : -1;
+}
+
 // pair (wave * ROUNDS + r) * 64 + lane of the share
 template <class S>
 __device__ __forceinline__ void load_pairs(PlanState<S>& s, const ExpertPlan& p, int64_t first) {
@@ -44,10 +52,7 @@ __device__ __forceinline__ void load_pairs(PlanState<S>& s, const ExpertPlan& p,
 #pragma unroll
   for (int r = 0; r < S::ROUNDS; ++r) {
     const int64_t i = first + (wave * S::ROUNDS + r) * 64 + lane;
-    int64_t id = -1;
-    if (i < p.pairs)
-      id = p.wide ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
-    s.e[r] = id >= 0 && id < p.experts ? (int)id : -1;
+    s.e[r] = i < p.pairs ? expert_of(p, i) : -1;
   }
 }
 
@@ -81,98 +86,152 @@ __device__ __forceinline__ void count_pairs(PlanState<S>& s, const ExpertPlan& p
   __syncthreads();
 }
 
+// Of the expert `threadIdx.x`, which has `total` pairs (0 past the last): the pairs of the
+// experts before, and of all in `sum`.
+template <class S>
+__device__ __forceinline__ int pairs_before(int total, int& sum) {
+  __shared__ int wave_sum[S::kWaves];
+  const int wave = threadIdx.x >> 6, upto = int_sums_of_wave(total);
+  if ((threadIdx.x & 63) == 63) wave_sum[wave] = upto;
+  __syncthreads();
+  int before = upto - total;
+  sum = 0;
+#pragma unroll
+  for (int w = 0; w < S::EXPERTS / 64; ++w) {
+    if (w < wave) before += wave_sum[w];
+    sum += wave_sum[w];
+  }
+  return before;
+}
+
+// The waves' counts of one expert become the places where each begins.
+template <class S>
+struct WaveCounts {
+  int n[S::kWaves], sum = 0;
+  __device__ __forceinline__ WaveCounts(const int* counts, int experts, int e) {
+#pragma unroll
+    for (int w = 0; w < S::kWaves; ++w) n[w] = counts[w * experts + e];
+#pragma unroll
+    for (int w = 0; w < S::kWaves; ++w) sum += n[w];
+  }
+  __device__ __forceinline__ void begin(int* counts, int experts, int e, int at) const {
+#pragma unroll
+    for (int w = 0; w < S::kWaves; ++w) {
+      counts[w * experts + e] = at;
+      at += n[w];
+    }
+  }
+};
+
+// One pair's outputs, `total` pairs having rows.
+__device__ __forceinline__ void place_pair(const ExpertPlan& p, int64_t i, int place, int total) {
+  if (place >= 0) p.rows[place] = (int32_t)((uint32_t)i / (uint32_t)p.top);
+  p.places[i] = place;
+  if (i >= total) p.rows[i] = -1;   // past the last row
+}
+
+// All pairs in one workgroup.
+template <class S>
+__global__ __launch_bounds__(S::THREADS) void expert_plan_kernel(const ExpertPlan p) {
+  __shared__ int counts[S::kWaves * S::EXPERTS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  PlanState<S> s;
+  load_pairs<S>(s, p, 0);
+  count_pairs<S>(s, p, counts);
+  const bool some = tid < p.experts;
+  const WaveCounts<S> n(counts, p.experts, some ? tid : 0);
+  int sum;
+  const int before = pairs_before<S>(some ? n.sum : 0, sum);
+  if (some) {
+    p.offsets[tid] = before;
+    n.begin(counts, p.experts, tid, before);
+  }
+  if (tid == 0) p.offsets[p.experts] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < S::ROUNDS; ++r) {
+    const int64_t i = (wave * S::ROUNDS + r) * 64 + lane;
+    if (i >= p.pairs) break;
+    place_pair(p, i, s.e[r] < 0 ? -1 : counts[wave * p.experts + s.e[r]] + s.at[r], sum);
+  }
+}
+
 template <class S>
 __global__ __launch_bounds__(S::THREADS) void expert_count_kernel(const ExpertPlan p) {
   __shared__ int counts[S::kWaves * S::EXPERTS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t first = (int64_t)blockIdx.x * S::kPairs;
   PlanState<S> s;
-  load_pairs<S>(s, p, (int64_t)blockIdx.x * S::kPairs);
+  load_pairs<S>(s, p, first);
   count_pairs<S>(s, p, counts);
-  for (int e = threadIdx.x; e < p.experts; e += S::THREADS) {
-    int n = 0;
+  if (tid < p.experts) {
+    const WaveCounts<S> n(counts, p.experts, tid);
+    n.begin(counts, p.experts, tid, 0);
+    p.counts[(int64_t)blockIdx.x * p.experts + tid] = n.sum;
+  }
+  __syncthreads();
 #pragma unroll
-    for (int w = 0; w < S::kWaves; ++w) n += counts[w * p.experts + e];
-    p.counts[(int64_t)blockIdx.x * p.experts + e] = n;
+  for (int r = 0; r < S::ROUNDS; ++r) {
+    const int64_t i = first + (wave * S::ROUNDS + r) * 64 + lane;
+    if (i >= p.pairs) break;
+    p.places[i] = s.e[r] < 0 ? -1 : counts[wave * p.experts + s.e[r]] + s.at[r];
   }
 }
 
 template <class S>
 __global__ __launch_bounds__(S::THREADS) void expert_place_kernel(const ExpertPlan p) {
-  __shared__ int counts[S::kWaves * S::EXPERTS];
   constexpr int kParts = S::THREADS / S::EXPERTS;   // threads that sum the workgroups' counts of an expert
   __shared__ int earlier[kParts][S::EXPERTS], all[kParts][S::EXPERTS];   // of the workgroups before, of all
-  __shared__ int wave_sum[S::kWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ int start[S::EXPERTS];
+  const int tid = threadIdx.x;
   const int64_t first = (int64_t)blockIdx.x * S::kPairs;
-  const int groups = gridDim.x;
-  PlanState<S> s;
-  load_pairs<S>(s, p, first);
-  // Plain sums of a thread, eight loads in flight: sums of a wave over its lanes took
-  // half of the kernel's time (32768 tokens x 8 of 256 experts: 17.5 -> 13.4 us).
-  const int part = tid / S::EXPERTS, mine = tid % S::EXPERTS;
-  if (groups > 1 && mine < p.experts) {
-    int sum = 0, before = 0;   // of the workgroups from this one on, of those before it
-    const int32_t* left = p.counts + mine;
-    int b = part;
-#pragma unroll 8
-    for (; b < (int)blockIdx.x; b += kParts) before += left[(int64_t)b * p.experts];
-#pragma unroll 8
-    for (; b < groups; b += kParts) sum += left[(int64_t)b * p.experts];
-    earlier[part][mine] = before;
-    all[part][mine] = before + sum;
-  }
-  count_pairs<S>(s, p, counts);
-
-  // sums over the experts, THREADS of them at a time
-  int before = 0;   // pairs of the experts of the rounds before
-  for (int e0 = 0; e0 < p.experts; e0 += S::THREADS) {
-    const int e = e0 + tid;
-    int n[S::kWaves], total = 0, at = 0;
-#pragma unroll
-    for (int w = 0; w < S::kWaves; ++w) n[w] = e < p.experts ? counts[w * p.experts + e] : 0;
-    if (groups > 1) {
-      if (e < p.experts)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-          at += earlier[i][e];
-          total += all[i][e];
-        }
-    } else {
-#pragma unroll
-      for (int w = 0; w < S::kWaves; ++w) total += n[w];
-    }
-    const int upto = int_sums_of_wave(total);
-    if (lane == 63) wave_sum[wave] = upto;
-    __syncthreads();
-    int base = before;
-#pragma unroll
-    for (int w = 0; w < S::kWaves; ++w) {
-      if (w < wave) base += wave_sum[w];
-      before += wave_sum[w];
-    }
-    if (e < p.experts) {
-      base += upto - total;
-      if (blockIdx.x == 0) p.offsets[e] = base;
-      at += base;
-#pragma unroll
-      for (int w = 0; w < S::kWaves; ++w) {
-        counts[w * p.experts + e] = at;
-        at += n[w];
-      }
-    }
-    __syncthreads();
-  }
-  if (blockIdx.x == 0 && tid == 0) p.offsets[p.experts] = before;
+  int e[S::ROUNDS], at[S::ROUNDS];
 #pragma unroll
   for (int r = 0; r < S::ROUNDS; ++r) {
-    const int64_t i = first + (wave * S::ROUNDS + r) * 64 + lane;
+    const int64_t i = first + r * S::THREADS + tid;
+    e[r] = i < p.pairs ? expert_of(p, i) : -1;
+    at[r] = i < p.pairs ? p.places[i] : 0;
+  }
+  // Plain sums of a thread, 16 loads in flight, then 4 (sums of a wave over its lanes
+  // took half of the kernel's time).
+  const int part = tid / S::EXPERTS, mine = tid % S::EXPERTS, groups = gridDim.x;
+  if (mine < p.experts) {
+    int sum = 0, before = 0, b = part;
+    const int32_t* left = p.counts + mine;
+    auto add = [&](int b) {
+      const int n = left[(int64_t)b * p.experts];
+      sum += n;
+      before += b < (int)blockIdx.x ? n : 0;
+    };
+    for (; b + 15 * kParts < groups; b += 16 * kParts)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) add(b + j * kParts);
+    for (; b + 3 * kParts < groups; b += 4 * kParts)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) add(b + j * kParts);
+    for (; b < groups; b += kParts) add(b);
+    earlier[part][mine] = before;
+    all[part][mine] = sum;
+  }
+  __syncthreads();
+  int total = 0, sum;
+  if (tid < p.experts)
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) total += all[i][tid];
+  int before = pairs_before<S>(total, sum);
+  if (tid < p.experts) {
+    if (blockIdx.x == 0) p.offsets[tid] = before;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) before += earlier[i][tid];
+    start[tid] = before;
+  }
+  if (blockIdx.x == 0 && tid == 0) p.offsets[p.experts] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < S::ROUNDS; ++r) {
+    const int64_t i = first + r * S::THREADS + tid;
     if (i >= p.pairs) break;
-    int place = -1;
-    if (s.e[r] >= 0) {
-      place = counts[wave * p.experts + s.e[r]] + s.at[r];
-      p.rows[place] = (int32_t)((uint32_t)i / (uint32_t)p.top);
-    }
-    p.places[i] = place;
-    if (i >= before) p.rows[i] = -1;   // past the last row
+    place_pair(p, i, e[r] < 0 ? -1 : start[e[r]] + at[r], sum);
   }
 }
 
@@ -257,28 +316,34 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const ExpertCombine
 
 template <class S>
 hipError_t launch_plan(const ExpertPlan& p, hipStream_t stream) {
-  const int64_t groups = cdiv(p.pairs, S::kPairs);
-  const dim3 grid((unsigned)(groups > 0 ? groups : 1));
-  if (groups > 1)
-    hipLaunchKernelGGL((expert_count_kernel<S>), grid, dim3(S::THREADS), 0, stream, p);
-  hipLaunchKernelGGL((expert_place_kernel<S>), grid, dim3(S::THREADS), 0, stream, p);
+  const dim3 grid((unsigned)cdiv(p.pairs, S::kPairs)), block(S::THREADS);
+  if (grid.x <= 1) {
+    hipLaunchKernelGGL((expert_plan_kernel<S>), dim3(1), block, 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((expert_count_kernel<S>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((expert_place_kernel<S>), grid, block, 0, stream, p);
+  }
   return hipGetLastError();
 }
 
-// Pairs of a workgroup.  One does up to 4096 (512 tokens x 8 of 128 experts 7.2 us; two
-// of 2048 with their second launch 8.3; 600 tokens: 8.4, with shares of 4096 11.7).
-// Above it shares of 2048 end soonest (2^14 pairs of 256 experts 9.4 us, 12.9 with
-// shares of 4096 and 20.2 with 8192; 2^18 13.5, 16.1, 23.4; 2^19 of 128 15.4, 17.1,
-// 22.7) until the sums over all the workgroups, in each of them, weigh more (2^20: 29.6,
-// 21.4, 25.7; 2^22 of 16: 187, 75, 50).
-constexpr int64_t kPlanAlone = 4096, kPlanMany = (int64_t)1 << 19, kPlanMost = (int64_t)1 << 20;
+// Pairs of a workgroup.  One does up to 2048 (256 tokens x 8 of 128 experts 4.6 us, in
+// two of 1024 with their second launch 5.4).  Above it small shares end soonest until
+// the sums over all the workgroups, in each of them, weigh more.  us with shares of
+// 1024 / 2048 / 4096 / 8192: 2^14 pairs of 256 experts 6.4 / 7.9 / 10.5 / 16.1, 2^16 of
+// 64 6.2 / 9.0 / 10.4 / 14.7, 2^18 of 256 11.5 / 11.2 / 13.5 / 21.0, 2^19 of 128 20.4 /
+// 13.4 / 14.7 / 21.7, 2^20 of 128 48 / 25.1 / 18.8 / 26.1, 2^21 146 / 58 / 35.7 / 38.4,
+// 2^22 of 256 665 / 205 / 88 / 68.
+constexpr int64_t kPlanAlone = 2048, kPlanFew = (int64_t)1 << 17, kPlanMany = (int64_t)1 << 19,
+                  kPlanMost = (int64_t)1 << 21;
 int64_t plan_share(int64_t pairs) {
-  return pairs <= kPlanAlone ? 4096 : pairs <= kPlanMany ? 2048 : pairs <= kPlanMost ? 4096 : 8192;
+  return pairs <= kPlanAlone ? 2048 : pairs <= kPlanFew ? 1024 : pairs <= kPlanMany ? 2048
+                                   : pairs <= kPlanMost ? 4096 : 8192;
 }
 
 template <int EXPERTS>
 hipError_t launch_plan_of(const ExpertPlan& p, hipStream_t stream) {
   switch (plan_share(p.pairs)) {
+    case 1024: return launch_plan<PlanShape<1024, 1, EXPERTS>>(p, stream);
     case 2048: return launch_plan<PlanShape<1024, 2, EXPERTS>>(p, stream);
     case 4096: return launch_plan<PlanShape<1024, 4, EXPERTS>>(p, stream);
     default: return launch_plan<PlanShape<1024, 8, EXPERTS>>(p, stream);
@@ -290,17 +355,20 @@ hipError_t launch_plan_of(const ExpertPlan& p, hipStream_t stream) {
 int64_t expert_plan_workspace(int64_t pairs, int64_t experts) {
   if (pairs <= kPlanAlone) return 0;
   // no less than fewer pairs need, so that one sized for the most serves them all
-  int64_t groups = cdiv(pairs, plan_share(pairs)), fewer = cdiv(pairs < kPlanMany ? pairs : kPlanMany, 2048);
-  if (groups < fewer) groups = fewer;
+  int64_t groups = 0;
+  for (const int64_t most : {kPlanFew, kPlanMany, kPlanMost, pairs}) {
+    const int64_t n = most < pairs ? most : pairs, g = cdiv(n, plan_share(n));
+    if (g > groups) groups = g;
+  }
   return groups * experts * (int64_t)sizeof(int);
 }
 
-// Few pairs take four waves (32 tokens x 8 of 128 experts: 5.1 -> 2.4 us, with one
-// round instead of eight).
+// Few pairs take four waves (32 tokens x 8 of 128 experts 2.4 us, with 16 waves 2.8), up
+// to 1024 one round of 16 waves (128 x 8 of 256 experts 3.5, four rounds of four 4.8).
 hipError_t launch_expert_plan(const ExpertPlan& p, hipStream_t stream) {
   if (p.experts > 256) return launch_plan_of<kMaxExperts>(p, stream);
   if (p.pairs <= 256) return launch_plan<PlanShape<256, 1, 256>>(p, stream);
-  if (p.pairs <= 1024) return launch_plan<PlanShape<256, 4, 256>>(p, stream);
+  if (p.pairs <= 1024) return launch_plan<PlanShape<1024, 1, 256>>(p, stream);
   return launch_plan_of<256>(p, stream);
 }
 

@@ -130,7 +130,7 @@ def test_sizes(lib):
         assert n(*bad) == ERR_SHAPE
     assert n(1, 0, (1 << 24) - 33, 0) == 0 and n(1, 0, (1 << 24) - 32, 0) == ERR_SHAPE
     w = lib.qgemm_expert_plan_workspace_bytes
-    assert w(0, 1) == 0 and w(4096, 1024) == 0 and w(4097, 7) == 3 * 7 * 4
+    assert w(0, 1) == 0 and w(2048, 1024) == 0 and w(2049, 7) == 3 * 7 * 4
     assert w(1 << 22, 1024) == (1 << 22) // 8192 * 1024 * 4
     # a workspace for the most pairs serves fewer
     sizes = [w(n, 7) for n in range(0, (1 << 22) + 1, 1024)] + [w(1 << 22, 7)]

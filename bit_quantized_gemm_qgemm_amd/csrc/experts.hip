@@ -123,9 +123,10 @@ struct WaveCounts {
   }
 };
 
-// One pair's outputs, `total` pairs having rows.
+// One pair's outputs, `total` pairs having rows.  (Calls that share a workspace at the
+// same time spoil each other's places, but write nothing outside the arrays.)
 __device__ __forceinline__ void place_pair(const ExpertPlan& p, int64_t i, int place, int total) {
-  if (place >= 0) p.rows[place] = (int32_t)((uint32_t)i / (uint32_t)p.top);
+  if ((uint32_t)place < (uint32_t)p.pairs) p.rows[place] = (int32_t)((uint32_t)i / (uint32_t)p.top);
   p.places[i] = place;
   if (i >= total) p.rows[i] = -1;   // past the last row
 }

@@ -504,7 +504,8 @@ int qgemm_w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_p
  * out is left as it was.)  rows NULL: row m reads row m of a and a_scale, and
  * a_rows is M.  Otherwise rows int32 [M] names the row, 0 .. a_rows - 1, that
  * each reads; one outside stands for codes and a scale of 0.  a_rows * K is below
- * 2^31.
+ * 2^31.  The work is shared out as if the experts had all M rows (the host does not
+ * know how many they have), so an M far above that costs time, not results.
  */
 int qgemm_w8a8_experts(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
                        const float* w_scale, const int32_t* offsets, const int32_t* rows, void* out,

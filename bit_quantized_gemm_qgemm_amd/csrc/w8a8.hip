@@ -198,9 +198,13 @@ __global__ __launch_bounds__(NW * kWave) void w8a8_slab_kernel(const Args g) {
             wr, 16u * lane + 1024u * h, (uint32_t)min(j, last) * stride + (uint32_t)kTileBytes * kt, 2);
   };
   // the weight does not wait for the row numbers
+  // (without K tiles: tile 0 of a buffer of 0 bytes, so nothing is read.  Tile -1 would be
+  // an offset of 4 GB - 2 KB in a scalar register, and the hardware compares a lane's offset
+  // with the buffer's size less the scalar one.)
+  const int last_kt = max(g.KT - 1, 0);
   SlabTile<G> ring[D];
 #pragma unroll
-  for (int d = 0; d < D; ++d) load_w(ring[d], min(wave + d * NW, g.KT - 1));
+  for (int d = 0; d < D; ++d) load_w(ring[d], min(wave + d * NW, last_kt));
 
   uint32_t xoff = kOutOfRange;
   float as = 0.f, ws = 0.f;
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(NW * kWave) void w8a8_slab_kernel(const Args g) {
       t.x[h] = __builtin_amdgcn_raw_buffer_load_b128(xr, xoff + 128u * kt + 16u * h, 0, 0);
   };
 #pragma unroll
-  for (int d = 0; d < D; ++d) load_x(ring[d], min(wave + d * NW, g.KT - 1));
+  for (int d = 0; d < D; ++d) load_x(ring[d], min(wave + d * NW, last_kt));
   auto load = [&](SlabTile<G>& t, int kt) {
     load_x(t, kt);
     load_w(t, kt);

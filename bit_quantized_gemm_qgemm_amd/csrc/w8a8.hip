@@ -34,6 +34,10 @@ struct Args {
   bool gated, bf16;
 };
 
+int64_t col_blocks(const W8a8& p, int64_t cols) {
+  return cdiv(w8a8_geom(p.K, p.N, p.gated).cg * kTileN, cols);
+}
+
 Args args_of(const W8a8& p, int64_t cols) {
   const W8a8Geom geom = w8a8_geom(p.K, p.N, p.gated);
   Args g;
@@ -54,7 +58,7 @@ Args args_of(const W8a8& p, int64_t cols) {
   g.CG = (int)geom.cg;
   g.KT = (int)geom.kt;
   g.w_bytes = geom.bytes;
-  g.col_blocks = (int)cdiv(geom.cg * kTileN, cols);
+  g.col_blocks = (int)col_blocks(p, cols);
   g.gated = p.gated;
   g.bf16 = p.bf16;
   return g;
@@ -64,6 +68,11 @@ Args args_of(const W8a8& p, int64_t cols) {
 int64_t most_row_blocks(const W8a8& p, int64_t rows) {
   if (!p.offsets) return cdiv(p.M, rows);
   return (p.M < p.experts ? p.M : p.experts) + p.M / rows;
+}
+
+// Workgroups of a launch: the items, an eighth of them for each XCD.
+int64_t workgroups(const W8a8& p, int64_t rows, int64_t cols) {
+  return cdiv(most_row_blocks(p, rows) * col_blocks(p, cols), 8) * 8;
 }
 
 // What a workgroup computes: rows m0 .. m0 + BM - 1 (those below hi) and one
@@ -300,8 +309,7 @@ __global__ __launch_bounds__(NW * kWave) void w8a8_slab_kernel(const Args g) {
 template <int G, int NW>
 hipError_t launch_slab(const W8a8& p, hipStream_t stream) {
   const Args g = args_of(p, 16 * G);
-  const int64_t items = most_row_blocks(p, 16) * g.col_blocks;
-  hipLaunchKernelGGL((w8a8_slab_kernel<G, NW>), dim3((unsigned)(cdiv(items, 8) * 8)),
+  hipLaunchKernelGGL((w8a8_slab_kernel<G, NW>), dim3((unsigned)workgroups(p, 16, 16 * G)),
                      dim3(NW * kWave), 0, stream, g);
   return hipGetLastError();
 }
@@ -683,9 +691,8 @@ __global__ __launch_bounds__(T::kThreads, T::kThreads > 256 ? 1 : 2) void w8a8_t
 template <class T>
 hipError_t launch_tile(const W8a8& p, hipStream_t stream) {
   const Args g = args_of(p, T::kCols);
-  const int64_t items = most_row_blocks(p, T::kRows) * g.col_blocks;
-  hipLaunchKernelGGL((w8a8_tile_kernel<T>), dim3((unsigned)(cdiv(items, 8) * 8)), dim3(T::kThreads), 0,
-                     stream, g);
+  hipLaunchKernelGGL((w8a8_tile_kernel<T>), dim3((unsigned)workgroups(p, T::kRows, T::kCols)),
+                     dim3(T::kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
@@ -704,29 +711,46 @@ hipError_t launch_tile(const W8a8& p, hipStream_t stream) {
 //   64 experts, K = 4096, N = 2048, 4 / 16 / 64 / 1024 rows each: 32 x 16 77 / 101
 //     / - / -, 128 x 32 99 (16), 128 x 64 115 (64), 256 x 128 497 (1024)
 struct Variant {
-  int rows, cols, ks;
+  int rows, cols, ks, threads;
   float fixed, step, shared, stream;
   hipError_t (*launch)(const W8a8&, hipStream_t);
 };
 
+template <int G, int NW>
+constexpr Variant slab(float fixed, float step, float shared, float stream) {
+  return {16, 16 * G, NW, NW * kWave, fixed, step, shared, stream, launch_slab<G, NW>};
+}
+template <int FM, int FN, int WR, int WC, int KS, int WB>
+constexpr Variant tile(float fixed, float step, float shared, float stream) {
+  using T = Tile<FM, FN, WR, WC, KS, WB>;
+  return {T::kRows, T::kCols, KS, T::kThreads, fixed, step, shared, stream, launch_tile<T>};
+}
+
 constexpr Variant kVariants[] = {
-    {16, 16, 8, 2.79f, 0.193f, 0.727f, 0.37f, launch_slab<1, 8>},   // not gated: one of a pair
-    {16, 32, 4, 3.00f, 0.382f, 0.517f, 0.36f, launch_slab<2, 4>},
-    {16, 64, 4, 2.82f, 0.746f, 0.907f, 0.57f, launch_slab<4, 4>},
-    {32, 32, 4, 3.29f, 0.320f, 0.561f, 1.14f, launch_tile<Tile<1, 1, 1, 1, 4, 4>>},
-    {32, 64, 4, 3.53f, 0.459f, 0.747f, 1.12f, launch_tile<Tile<1, 1, 1, 2, 4, 2>>},
-    {32, 128, 1, 3.52f, 0.169f, 0.287f, 1.13f, launch_tile<Tile<1, 1, 1, 4, 1, 4>>},
-    {64, 64, 2, 4.21f, 0.289f, 0.499f, 1.06f, launch_tile<Tile<2, 1, 1, 2, 2, 4>>},
-    {64, 128, 1, 3.77f, 0.223f, 0.377f, 1.07f, launch_tile<Tile<2, 1, 1, 4, 1, 4>>},
-    {128, 128, 1, 5.09f, 0.000f, 0.551f, 1.14f, launch_tile<Tile<4, 1, 1, 4, 1, 4>>},
-    {96, 256, 1, 5.93f, 0.142f, 0.751f, 1.33f, launch_tile<Tile<3, 2, 1, 4, 1, 2>>},
-    {128, 256, 1, 7.11f, 0.544f, 0.905f, 1.26f, launch_tile<Tile<4, 2, 1, 4, 1, 2>>},
-    {256, 256, 1, 6.98f, 1.039f, 1.744f, 0.86f, launch_tile<Tile<4, 2, 2, 4, 1, 2>>},
+    slab<1, 8>(2.79f, 0.193f, 0.727f, 0.37f),               // 16 x 16; not gated: one of a pair
+    slab<2, 4>(3.00f, 0.382f, 0.517f, 0.36f),               // 16 x 32
+    slab<4, 4>(2.82f, 0.746f, 0.907f, 0.57f),               // 16 x 64
+    tile<1, 1, 1, 1, 4, 4>(3.29f, 0.320f, 0.561f, 1.14f),   // 32 x 32
+    tile<1, 1, 1, 2, 4, 2>(3.53f, 0.459f, 0.747f, 1.12f),   // 32 x 64
+    tile<1, 1, 1, 4, 1, 4>(3.52f, 0.169f, 0.287f, 1.13f),   // 32 x 128
+    tile<2, 1, 1, 2, 2, 4>(4.21f, 0.289f, 0.499f, 1.06f),   // 64 x 64
+    tile<2, 1, 1, 4, 1, 4>(3.77f, 0.223f, 0.377f, 1.07f),   // 64 x 128
+    tile<4, 1, 1, 4, 1, 4>(5.09f, 0.000f, 0.551f, 1.14f),   // 128 x 128
+    tile<3, 2, 1, 4, 1, 2>(5.93f, 0.142f, 0.751f, 1.33f),   // 96 x 256
+    tile<4, 2, 1, 4, 1, 2>(7.11f, 0.544f, 0.905f, 1.26f),   // 128 x 256
+    tile<4, 2, 2, 4, 1, 2>(6.98f, 1.039f, 1.744f, 0.86f),   // 256 x 256
 };
 
 // Of rows that fall on the experts at random: how many experts have any.
 double busy_experts(const W8a8& p) {
   return p.offsets ? (double)p.experts * (1 - std::exp(-(double)p.M / (double)p.experts)) : 1;
+}
+
+// A launch holds less than 2^32 threads in one dimension of its grid.  Of many columns and
+// rows that many experts share a small tile has more; the one of 128 x 256 never has: with
+// M N < 2^31 and up to M row blocks more than full ones, 2^23 workgroups of 256 threads.
+bool fits_a_launch(const Variant& v, const W8a8& p) {
+  return workgroups(p, v.rows, v.cols) * v.threads < (int64_t)1 << 32;
 }
 
 double estimate(const Variant& v, const W8a8& p, double busy) {
@@ -754,7 +778,7 @@ const Variant& variant_for(const W8a8& p) {
   for (const Variant& v : kVariants) {
     if ((v.rows == 16 && !few) || (v.cols == 16 && p.gated)) continue;
     const double t = estimate(v, p, busy);
-    if (!best || t < least) {
+    if ((!best || t < least) && fits_a_launch(v, p)) {
       best = &v;
       least = t;
     }

@@ -66,3 +66,15 @@ def test_by_expert(counts, N, gated, dtype):
     owned = np.zeros(M, bool)
     owned[lead:M - tail] = True
     same(out, expected(M, N, gated, scales, owned))
+
+
+def test_many_rows_of_many_experts():
+    """65536 rows of 1024 experts by 32767 columns: of the smallest tile the launch would have
+    2^32 threads and more."""
+    print("case w8a8 no k, many", flush=True)
+    M, N, E = 65536, 32767, 1024
+    out = torch.full((M, N), 7.0, dtype=torch.float16, device="cuda")
+    offsets = torch.arange(E + 1, device="cuda", dtype=torch.int32) * (M // E)
+    qg.qgemm_w8a8_experts(i8(M, 0), torch.ones(M, device="cuda"), qg.qgemm_prepack_w8a8(i8(E, 0, N)),
+                          torch.ones((E, N), device="cuda"), offsets, N, out=out)
+    assert (out == 0).all()

@@ -359,7 +359,7 @@ constexpr int64_t kMaxInt8K = 131056;
 constexpr int64_t kMaxInt8Rows = (int64_t)1 << 28;
 
 // One packed weight stays below 2^31 bytes (32-bit offsets within it), all of
-// them below 2^40.
+// them below 2^41.
 int check_w8a8_weight(int64_t experts, int64_t K, int64_t N, int gated) {
   if (!below(experts, 1, qgemm::kMaxExperts + 1) || !below(K, 0, kMaxInt8K + 1) || K % 16 != 0 ||
       !below(N, 0, kMaxIndex) || (gated != 0 && gated != 1) || (gated && N % 2 != 0))

@@ -701,10 +701,13 @@ hipError_t launch_tile(const W8a8& p, hipStream_t stream) {
 // item (a workgroup's tile) runs through K in steps of KS K tiles of 128; a step
 // takes `step` us, or `shared` us for each item that a CU works on where that is
 // more; the weight's bytes stream beside that at 6.9 TB/s and show with the factor
-// `stream`; `fixed` us go before and after.  The figures are fitted to 246 sizes
-// timed with every variant (N 640 .. 28672, K 1024 .. 8192, 1 .. 4096 rows; 8 .. 128
-// experts of 1 .. 1024 rows on average).  Over these the choice is 1.1 % slower than
-// the best variant of each in the mean, 17 % at worst.  Single sizes, us:
+// `stream`; `fixed` us go before and after.  The figures are fitted to 236 sizes of
+// plain products in bf16 (N 640 .. 28672, K 1024 .. 8192; 161 of 1 .. 4096 rows, 75 of
+// 8 .. 128 experts with 1 .. 1024 rows on average), each timed with those 5 to 12 of the
+// variants that come into question for so many rows.  Over these the choice is 0.8 %
+// slower than the best timed (0.3 % with one weight, 2.1 % by expert), 17 % at worst.
+// Gated products and sizes outside these ranges follow the same rule unmeasured, but for
+// some (4096 x 11008 gated, 16 .. 512 rows: 0 to 6 % less than plain).  Single sizes, us:
 //   K = N = 8192, 16 / 64 / 256 / 1024 / 4096 rows: 32 columns by 16 rows 12.9 /
 //     26.9, 64 x 32 20.0 / 19.7 (32 and 64 rows), 128 x 64 30.7 (256), 256 x 128
 //     64.3 (1024), 256 x 256 213 (4096; 256 x 128 219, 128 x 128 260)
@@ -787,7 +790,7 @@ const Variant& variant_for(const W8a8& p) {
 }
 
 // ---- prepack ----------------------------------------------------------------
-// One thread per 32-bit word of the packed weight, grid z over experts.
+// One thread per 32-bit word of the packed weight, grid y over experts.
 __global__ __launch_bounds__(256) void prepack_w8a8_kernel(const int8_t* __restrict__ w,
                                                            uint32_t* __restrict__ out, int K, int N,
                                                            int KT, int64_t words, bool gated) {

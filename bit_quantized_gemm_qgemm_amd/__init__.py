@@ -815,7 +815,8 @@ def qgemm_w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows=None, gat
     w_packed is of [experts, K, N], w_scale float32 [experts, N], offsets int32
     [experts + 1].  rows, int32 [M], names the row of a (and a_scale) that each
     of the M output rows reads; without it row m reads row m.  Rows that no
-    expert has are left as they were."""
+    expert has are not written: in `out` they stay as they were, and in the new
+    tensor that a call without `out` returns they hold whatever its memory held."""
     status = None
     if _native and out is not None:
         status = _native.w8a8_experts(a, a_scale, w_packed, w_scale, offsets, N, rows, gated, out)

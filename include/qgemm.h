@@ -488,8 +488,9 @@ int qgemm_prepack_w8a8(const int8_t* w, void* w_packed, int64_t experts, int64_t
  * a: int8 [M, K], any codes; a_scale fp32 [M]; w_packed from qgemm_prepack_w8a8
  * with the same K, N and gated; w_scale fp32 [N]; out: dtype (QGEMM_F16 or
  * QGEMM_BF16).  The sum is exact; it is rounded to fp32, multiplied by a_scale
- * and then by w_scale in fp32, and the result is rounded once.  M is below 2^28,
- * M * K and M * N below 2^31.
+ * and then by w_scale in fp32, and the result is rounded once.  silu is formed in
+ * fp32 too: below y = -87.3, where exp(-y) nears fp32's largest value, it is 0.
+ * M is below 2^28, M * K and M * N below 2^31.
  */
 int qgemm_w8a8(int dtype, const int8_t* a, const float* a_scale, const void* w_packed,
                const float* w_scale, void* out, int64_t M, int64_t N, int64_t K, int gated,
